@@ -1,4 +1,4 @@
-"""ctypes binding of libdg (include/dg.h): argument marshalling only.
+"""ctypes binding of libdg (include/dg.h, include/dg_paged.h): argument marshalling only.
 
 Every function below forwards to the C entry point of the same name; device
 buffers are passed as torch CUDA tensors (PyTorch supplies device memory and
@@ -12,6 +12,10 @@ acceptance of the lowest-entropy prefix, re-noising of the rest), as one forward
 or as the whole loop; and self-conditioning, where the tensor z that a forward
 leaves behind is fed into the canvas input of the next one.  Tensors for z hold
 the model's accumulate type: fp64 for the f32 model, fp32 for the bf16 ones.
+
+Apart from these, the paged-cache operators (dg_qk_norm_rope, dg_paged_append,
+dg_paged_attention) need no model: PagedCache and PagedBatch describe the caller's
+tensors.
 """
 from __future__ import annotations
 
@@ -60,6 +64,30 @@ class dg_weights(ctypes.Structure):
                 ("layers", ctypes.POINTER(dg_layer_weights)), ("sc_gate", ctypes.c_void_p),
                 ("sc_up", ctypes.c_void_p), ("sc_down", ctypes.c_void_p)]
 
+
+class dg_heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("n_heads", ctypes.c_int32)]
+
+
+class dg_rope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * 128)]
+
+
+class dg_paged_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("dtype", "n_pages", "page_size", "n_kv_heads",
+                                      "head_dim")] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "token_stride", "head_stride")]
+
+
+class dg_paged_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "n_tokens", "max_q", "max_pages")] + [
+        (n, ctypes.c_void_p) for n in ("q_start", "kv_len", "page_table")]
+
+
+_ELEMS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # dg_elem
 
 _lib = None
 
@@ -140,6 +168,12 @@ def lib() -> ctypes.CDLL:
             "dg_anneal_init": [vp, vp, vp, i32, i32, i32, vp, vp],
             "dg_set_selfcond": [vp, i32],
             "dg_selfcond_forward": [vp, vp, vp, i32, i32, vp, vp, vp, vp, vp],
+            "dg_rope_init": [ctypes.c_double, i32, vp],
+            "dg_qk_norm_rope": [i32, i32, i32, vp, vp, vp, vp, vp, vp, f32, vp, vp, vp],
+            "dg_paged_append": [vp, vp, vp, vp, vp, vp, f32, vp, vp, vp, vp, vp],
+            "dg_paged_attention_workspace": [vp, vp, i32, ctypes.POINTER(ctypes.c_size_t)],
+            "dg_paged_attention": [vp, vp, vp, i32, vp, i32, f32, vp, vp, vp,
+                                   ctypes.c_size_t, vp, vp],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -159,7 +193,9 @@ def exported_symbols():
                         "dg_debug_stall_experts", "dg_prefill_into", "dg_append_block",
                         "dg_generate_blocks", "dg_generate_block_annealed",
                         "dg_anneal_forward", "dg_anneal_sample", "dg_anneal_init",
-                        "dg_set_selfcond", "dg_selfcond_forward")
+                        "dg_set_selfcond", "dg_selfcond_forward", "dg_rope_init",
+                        "dg_qk_norm_rope", "dg_paged_append", "dg_paged_attention_workspace",
+                        "dg_paged_attention")
             if hasattr(lib(), n)]
 
 
@@ -579,3 +615,213 @@ def dg_block_loop_launches(model: Model) -> int:
 def dg_debug_stall_experts(model: Model, limit_ns: int):
     """Test hook: the next routed-expert launch runs its waits out after limit_ns."""
     _check(lib().dg_debug_stall_experts(model.handle, limit_ns))
+
+
+# ---- paged cache (include/dg_paged.h) ----------------------------------------------
+
+PAGED_BAD_BATCH, PAGED_BAD_PAGE, PAGED_TIMEOUT = 1, 2, 4  # bits of an err word
+
+
+def _cuda(t, name: str, dtype, ndim: int):
+    """A caller tensor of this type (or one of these) and rank on the current device."""
+    if not torch.is_tensor(t):
+        raise ValueError(f"{name} must be a tensor")
+    if t.dim() != ndim or (t.dtype not in dtype if isinstance(dtype, (tuple, dict))
+                           else t.dtype != dtype):
+        raise ValueError(f"{name} must be a {ndim}-D tensor of {dtype}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    return t
+
+
+def _heads(t, name: str, dtype, n=None, h=None) -> dg_heads:
+    """dg_heads of a [rows, heads, channels] tensor: any row and head strides, contiguous
+    channels."""
+    _cuda(t, name, dtype, 3)
+    if (n is not None and t.shape[0] != n) or (h is not None and t.shape[2] != h):
+        raise ValueError(f"{name} must have {n} rows of {h} channels a head, got "
+                         f"{tuple(t.shape)}")
+    st = t.stride()
+    if t.shape[2] > 1 and st[2] != 1 and t.numel():
+        raise ValueError(f"{name} must have contiguous channels")
+    return dg_heads(t.data_ptr(), st[0], st[1], t.shape[1])
+
+
+def _gain(t, name: str, dtype, h: int):
+    return None if t is None else _arg(t, name, dtype, (h,))
+
+
+def _err(t):
+    return _arg(t, "err", torch.int32, (1,))
+
+
+def _empty(stream, *shape, dtype):
+    """A tensor whose memory belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device="cuda")
+
+
+class PagedCache:
+    """One layer's pages: k_pages and v_pages [n_pages, page_size, Hkv, h], bf16 or f16,
+    of equal strides.  Any order of the first three axes in memory will do (a permuted
+    view, say); the channels are contiguous.  Keeps the tensors, copies nothing."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor):
+        _cuda(k_pages, "k_pages", (torch.bfloat16, torch.float16), 4)
+        _cuda(v_pages, "v_pages", k_pages.dtype, 4)
+        if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+            raise ValueError("k_pages and v_pages must have the same shape and strides")
+        if k_pages.stride(3) != 1:
+            raise ValueError("pages must have contiguous channels")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        n, ps, hkv, h = k_pages.shape
+        sp, st, sh, _ = k_pages.stride()
+        self.n_kv_heads, self.head_dim, self.page_size = hkv, h, ps
+        self.c = dg_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), _ELEMS[self.dtype], n,
+                                ps, hkv, h, sp, st, sh)
+
+
+class PagedBatch:
+    """The sequences of a call: q_start [B + 1], kv_len [B] and page_table [B, max_pages],
+    int32 on the device, and max_q, a host bound on the chunks' lengths.  The device
+    values are read by each call when it runs, so one PagedBatch serves a captured graph
+    whose tensors are updated between replays."""
+
+    def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                 max_q: int):
+        _cuda(page_table, "page_table", torch.int32, 2)
+        B, width = page_table.shape
+        _arg(kv_len, "kv_len", torch.int32, (B,))
+        _arg(q_start, "q_start", torch.int32, (B + 1,))
+        _arg(page_table, "page_table", torch.int32, (B, width))
+        if max_q < 0 or max_q > 0x7fffffff:
+            raise ValueError("max_q outside [0, 2^31)")
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.B, self.max_q, self.max_pages = B, int(max_q), width
+        self._p = (q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr())
+        self.device = page_table.device
+
+    def c(self, n_tokens: int) -> dg_paged_batch:
+        return dg_paged_batch(self.B, n_tokens, self.max_q, self.max_pages, *self._p)
+
+
+def dg_rope_init(base: float, head_dim: int) -> dg_rope:
+    """The constants of a rotation by position * base^(-2i/head_dim) (host memory)."""
+    r = dg_rope()
+    _check(lib().dg_rope_init(base, head_dim, ctypes.byref(r)))
+    return r
+
+
+def _eps(eps) -> float:
+    if eps is None:
+        return -1.0
+    if not eps >= 0:
+        raise ValueError("eps must be >= 0 (None: no norm)")
+    return eps
+
+
+def _opt_ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def dg_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions=None, rope: dg_rope | None = None,
+                    q_gain=None, k_gain=None, eps: float | None = 1e-6, q_out=None, k_out=None,
+                    stream=None):
+    """RMSNorm of every head row of q [n, Hq, h] and k [n, Hkv, h] (times q_gain and
+    k_gain [h]; eps None: no norm), then the rotation to positions [n] int32 (rope None:
+    none), in one pass.  bf16, f16 or f32; any row and head strides; q_out and k_out may be
+    q and k.  Returns (q_out, k_out)."""
+    qh = _heads(q, "q", _ELEMS)
+    n, _, h = q.shape
+    kh = _heads(k, "k", q.dtype, n, h)
+    if q_out is None:
+        q_out = _empty(stream, q.shape, dtype=q.dtype)
+    if k_out is None:
+        k_out = _empty(stream, k.shape, dtype=k.dtype)
+    qo, ko = _heads(q_out, "q_out", q.dtype, n, h), _heads(k_out, "k_out", q.dtype, n, h)
+    _check(lib().dg_qk_norm_rope(
+        _ELEMS[q.dtype], n, h, ctypes.byref(qh), ctypes.byref(kh),
+        _arg(positions, "positions", torch.int32, (n,)), _opt_ref(rope),
+        _gain(q_gain, "q_gain", q.dtype, h), _gain(k_gain, "k_gain", q.dtype, h), _eps(eps),
+        ctypes.byref(qo), ctypes.byref(ko), _stream(stream)))
+    return q_out, k_out
+
+
+def _same_device(*xs):
+    d = torch.cuda.current_device()
+    for x in xs:
+        if x.device.index != d:
+            raise ValueError("the cache and the batch must be on the current device")
+
+
+def dg_paged_append(cache: PagedCache, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor,
+                    rope: dg_rope | None = None, k_gain=None, eps: float | None = None, q=None,
+                    q_gain=None, q_out=None, err=None, stream=None):
+    """Stores the chunk rows' keys k [n, Hkv, h] (normalised if eps is given, rotated to
+    their positions if rope is) and values v into their pages; with q [n, Hq, h] also
+    writes the normalised and rotated queries to q_out (may be q).  Returns q_out.
+    err: a device int32 [1] that collects PAGED_BAD_* bits (dg_paged_check)."""
+    _same_device(cache, batch)
+    h, dt = cache.head_dim, cache.dtype
+    kh = _heads(k, "k", dt, None, h)
+    n = k.shape[0]
+    vh = _heads(v, "v", dt, n, h)
+    qh = qo = None
+    if q is not None:
+        qh = _heads(q, "q", dt, n, h)
+        if q_out is None:
+            q_out = _empty(stream, q.shape, dtype=dt)
+    if q_out is not None:
+        qo = _heads(q_out, "q_out", dt, n, h)
+    b = batch.c(n)
+    _check(lib().dg_paged_append(
+        ctypes.byref(cache.c), ctypes.byref(b), ctypes.byref(kh), ctypes.byref(vh),
+        _opt_ref(rope), _gain(k_gain, "k_gain", dt, h), _eps(eps), _opt_ref(qh),
+        _gain(q_gain, "q_gain", dt, h), _opt_ref(qo), _err(err), _stream(stream)))
+    return q_out
+
+
+def dg_paged_attention(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, causal=True,
+                       window: int = 0, scale: float | None = None, out=None, lse=None,
+                       err=None, stream=None):
+    """Attention of the chunk rows q [n, Hq, h] over their sequences' pages; returns out
+    [n, Hq, h].  causal: a bool, or a uint8 flag per sequence [B] (0: the chunk's rows see
+    the whole chunk).  window: the positions back a causal row sees, itself included, or
+    that a bidirectional chunk sees before itself (0: all).  scale: 1 / sqrt(h) unless
+    given.  lse: float32 [n, Hq] to receive the log of each row's sum of exponentials."""
+    _same_device(cache, batch)
+    h, dt = cache.head_dim, cache.dtype
+    qh = _heads(q, "q", dt, None, h)
+    n, hq, _ = q.shape
+    flags = None
+    if torch.is_tensor(causal):
+        flags, causal = _arg(causal, "causal", torch.uint8, (batch.B,)), True
+    b = batch.c(n)
+    need = ctypes.c_size_t()
+    _check(lib().dg_paged_attention_workspace(ctypes.byref(cache.c), ctypes.byref(b), hq,
+                                              ctypes.byref(need)))
+    if out is None:
+        out = _empty(stream, n, hq, h, dtype=dt)
+    ws = _empty(stream, need.value, dtype=torch.uint8)
+    _check(lib().dg_paged_attention(
+        ctypes.byref(cache.c), ctypes.byref(b), ctypes.byref(qh), 1 if causal else 0, flags,
+        window, h ** -0.5 if scale is None else scale, _arg(out, "out", dt, (n, hq, h)),
+        _arg(lse, "lse", torch.float32, (n, hq)), ws.data_ptr(), need.value, _err(err),
+        _stream(stream)))
+    return out
+
+
+def dg_paged_check(err: torch.Tensor):
+    """Reads an err word (synchronising) and raises DGError if a bit is set."""
+    _err(err)
+    bits = int(err.item())
+    if bits & PAGED_TIMEOUT:
+        raise DGError(5, lib().dg_status_str(5).decode(), "a bounded device-side wait gave up")
+    if bits:
+        what = [t for f, t in ((PAGED_BAD_BATCH, "a sequence's q_start or kv_len is out of range"),
+                               (PAGED_BAD_PAGE, "a page number is out of range")) if bits & f]
+        raise DGError(1, lib().dg_status_str(1).decode(), "; ".join(what))

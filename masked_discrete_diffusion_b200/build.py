@@ -8,7 +8,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libdg.so")
-SOURCES = ["dg_api.cu", "tc_host.cu", "noalloc.cu"]
+SOURCES = ["dg_api.cu", "tc_host.cu", "noalloc.cu", "paged.cu"]
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-lineinfo",
          "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr"]
 
@@ -25,7 +25,7 @@ def needs_build() -> bool:
         return True
     t = os.path.getmtime(OUT)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(HERE, "..", "include", "dg.h"))
+    deps += [os.path.join(HERE, "..", "include", f) for f in ("dg.h", "dg_paged.h")]
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 
