@@ -1,22 +1,53 @@
 // Attention of chunks of new tokens over a cache in pages (include/dg_paged.h:
-// dg_paged_attention).
+// dg_paged_attention) on tcgen05.
 //
-// One warp per (row, query head): a pass over the visible keys with the running maximum m
-// and sum l of the softmax, o = o 2^(m_old - m) + 2^(s - m) v.  Simple and right for every
-// shape; each key is read again by every row.
+//   out = softmax(scale Q K^T) V, one pass over the keys with the running maximum m and sum
+//   l of each row; P = 2^(s - m) is unnormalised and the division comes last.
+//
+// Rows.  The G = Hq / Hkv query heads of a key head share its keys, so a tile's 128 rows are
+// T = 128 / G tokens times G heads, and a single token fills G rows.  An ITEM is a sequence,
+// a key head and up to 2 T tokens, with the key tiles (128 keys) that any of its rows sees.
+// With more than T tokens its two row tiles take every key tile (a PAIR); with fewer its one
+// row tile is computed as two streams, the even and the odd key tiles (SOLO), and the two
+// meet at the end.  Either way two softmax warpgroups work while the tensor cores fill the
+// other's scores.
+//
+// Split.  All items' key tiles form one line; 148 CTAs take equal contiguous parts of it, so
+// no length mix leaves SMs idle.  A CTA's part is a run of whole items with a cut one at
+// either end; cut pieces leave (m, l, O) in the workspace and paged_merge_kernel adds an
+// item's pieces in the order of the line (the same bits every time).  Each CTA finds its
+// part from the lengths on the device: no host plan, and a captured graph follows them.
+//
+// CTA.  Warps 0-3 and 4-7: the streams' softmax, a thread a row (TMEM lane = row).  Warp 8:
+// MMA issue.  Warp 9: TMA.  S (128 columns) and O of both streams fill TMEM; P takes S's
+// place as the A operand of O += P V.  K and V tiles pass through one ring of slots in the
+// order of their first use.  O is rescaled only when a row's maximum has grown by 2^8, by
+// its own warp; until then P's exponents are taken against the older maximum, which the
+// final division cancels.
 #pragma once
 
 #include "k_paged_rows.cuh"
+#include "tc_ptx.cuh"
 
 namespace dg {
 
+constexpr int PA_CTAS = 148;
+constexpr int PA_THREADS = 384;  // 12 warps: 8 softmax, MMA, TMA, 2 that only help to plan
+constexpr int PA_KT = 128;                 // keys a tile
+constexpr uint32_t PA_CHUNK = 128 * 128;   // 128 rows of 64 channels
+
+template <int H> struct PagedCfg {
+  static constexpr int CH = H / 64;                 // 64-channel chunks
+  static constexpr uint32_t TILE = CH * PA_CHUNK;   // a Q, K or V tile
+  static constexpr int SLOTS = H == 128 ? 4 : 8;
+  static constexpr size_t SMEM =
+      1024 + (2 + SLOTS) * TILE + 512 /* barriers, plan */ + 2 * 128 * 8 /* m, l */;
+};
+
 struct PagedAttnParams {
-  const char *k, *v;
-  long long ps, ts, hs;  // page, token and head strides in bytes
   int page_log2, n_pages, max_pages, B, n, max_q;
   const int32_t *q_start, *kv_len, *table;
-  HeadsDev q;
-  int hq, hkv;
+  int hq, hkv, G, T;
   int causal;
   const uint8_t* causal_seq;
   int window;
@@ -24,68 +55,755 @@ struct PagedAttnParams {
   void* out;
   float* lse;
   int32_t* err;
+  // workspace
+  int part_rows;  // rows of a piece
+  float* part_o;  // [PA_CTAS][2][part_rows][H]
+  float2* part_ml;  // [PA_CTAS][2][part_rows]
+  struct PagedRec* rec;  // [PA_CTAS]
 };
 
-template <class T, int H>
-__global__ void __launch_bounds__(256) paged_attn_rows_kernel(const PagedAttnParams p) {
-  pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(w / p.hq), j = (int)(w % p.hq);
-  if (t >= p.n) return;
-  const int b = find_seq(p.q_start, p.B, t, lane);
-  if (b >= p.B) return;
+// An item whose first piece is CTA c's second slot; the others are the first slots of
+// c + 1 .. last.
+struct PagedRec {
+  int valid, last, row0, ntok, g, pad_[3];
+};
+
+struct PagedSeq {
+  int b, q0, ql, past, kv, causal;
+};
+
+// Sequence b, with ql = 0 where its numbers are out of range (true then).
+__device__ __forceinline__ bool paged_seq(const PagedAttnParams& p, int b, PagedSeq* s) {
   const int q0 = p.q_start[b], q1 = p.q_start[b + 1], kv = p.kv_len[b];
-  if (t < q0) return;
-  if (q0 < 0 || q1 > p.n || q1 <= t || q1 - q0 > p.max_q || kv < 0 ||
-      kv > (long long)p.max_pages << p.page_log2) {
-    if (lane == 0 && p.err) atomicOr(p.err, DG_PAGED_BAD_BATCH);
-    return;
+  s->b = b;
+  s->q0 = q0;
+  s->kv = kv;
+  const bool bad = q0 < 0 || q1 < q0 || q1 > p.n || q1 - q0 > p.max_q || kv < 0 ||
+                   kv > (long long)p.max_pages << p.page_log2;
+  s->ql = bad ? 0 : q1 - q0;
+  s->past = bad ? 0 : kv - s->ql;
+  s->causal = p.causal_seq ? p.causal_seq[b] != 0 : p.causal != 0;
+  return bad;
+}
+
+// Keys [lo, hi) that tokens i0 .. i0 + nt - 1 of the sequence see between them, and the tile
+// range [t0, t0 + n) that holds them (one tile, seen by nobody, if there are none).
+struct PagedKeys {
+  int lo, hi, t0, n;
+};
+__device__ __forceinline__ PagedKeys paged_keys(const PagedAttnParams& p, const PagedSeq& s,
+                                                int i0, int nt) {
+  PagedKeys k;
+  k.hi = s.causal ? min(s.kv, s.past + i0 + nt) : s.kv;
+  k.lo = 0;
+  if (p.window) {
+    const long long lo = (long long)(s.causal ? s.past + i0 + 1 : s.past) - p.window;
+    k.lo = lo > 0 ? (int)lo : 0;
   }
-  const int past = kv - (q1 - q0), pos = past + (t - q0);
-  const bool causal = p.causal_seq ? p.causal_seq[b] != 0 : p.causal != 0;
-  const int hi = causal ? min(kv, pos + 1) : kv;
-  const int lo = p.window ? max(0, (causal ? pos + 1 : past) - p.window) : 0;
-  constexpr int D = H / 32;
-  const int g = j / (p.hq / p.hkv);
-  float q[D], o[D];
-  const T* qp = reinterpret_cast<const T*>(p.q.p + t * p.q.ts + j * p.q.hs) + D * lane;
-#pragma unroll
-  for (int i = 0; i < D; ++i) {
-    q[i] = widen(qp[i]) * p.scale_log2;
-    o[i] = 0.f;
+  if (k.hi <= k.lo) {
+    k.lo = k.hi = k.t0 = 0;
+    k.n = 1;
+  } else {
+    k.t0 = k.lo / PA_KT;
+    k.n = (k.hi - 1) / PA_KT + 1 - k.t0;
   }
-  float m = -INFINITY, l = 0.f;
-  bool bad = false;
-  for (int s = lo; s < hi; ++s) {
-    const int page = p.table[(long long)b * p.max_pages + (s >> p.page_log2)];
-    if (page < 0 || page >= p.n_pages) {
-      bad = true;
-      break;
+  return k;
+}
+
+__device__ __forceinline__ long long paged_work(const PagedAttnParams& p, const PagedSeq& s) {
+  long long w = 0;
+  for (int i0 = 0; i0 < s.ql; i0 += 2 * p.T)
+    w += paged_keys(p, s, i0, min(2 * p.T, s.ql - i0)).n;
+  return w * p.hkv;
+}
+
+// Walks the pieces of a CTA's part of the line.
+struct PagedWalk {
+  PagedSeq s;
+  PagedKeys k;
+  int i0, nt;    // the item's tokens
+  int g;         // its key head
+  int off;       // tiles of it that lie before
+  long long left;
+  // the current piece
+  int first, count;
+
+  __device__ __forceinline__ void item(const PagedAttnParams& p) {
+    nt = min(2 * p.T, s.ql - i0);
+    k = paged_keys(p, s, i0, nt);
+  }
+  __device__ __forceinline__ void start(const PagedAttnParams& p, int b, long long skip,
+                                        long long count_) {
+    left = count_;
+    if (left <= 0) return;
+    paged_seq(p, b, &s);
+    i0 = 0;
+    item(p);
+    while (skip >= (long long)k.n * p.hkv && i0 + 2 * p.T < s.ql) {
+      skip -= (long long)k.n * p.hkv;
+      i0 += 2 * p.T;
+      item(p);
     }
-    const long long at =
-        page * p.ps + (s & ((1 << p.page_log2) - 1)) * p.ts + g * p.hs + D * lane * sizeof(T);
-    const T* kp = reinterpret_cast<const T*>(p.k + at);
-    const T* vp = reinterpret_cast<const T*>(p.v + at);
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < D; ++i) x += q[i] * widen(kp[i]);
-    x = warp_sum(x);
-    const float mn = fmaxf(m, x), a = exp2f(m - mn), e = exp2f(x - mn);
-    l = l * a + e;
-#pragma unroll
-    for (int i = 0; i < D; ++i) o[i] = o[i] * a + e * widen(vp[i]);
-    m = mn;
+    g = (int)(skip / k.n);
+    off = (int)(skip % k.n);
   }
-  if (bad && lane == 0 && p.err) atomicOr(p.err, DG_PAGED_BAD_PAGE);
-  const float nan = __int_as_float(0x7fc00000);
-  const float inv = bad ? nan : l == 0.f ? 0.f : 1.f / l;
-  T* op = reinterpret_cast<T*>(p.out) + ((long long)t * p.hq + j) * H + D * lane;
+  // Prepares the next piece; false at the end of the part.
+  __device__ __forceinline__ bool next(const PagedAttnParams& p) {
+    if (left <= 0) return false;
+    if (off == k.n) {  // the item is done: next head, tokens, sequence
+      off = 0;
+      if (++g == p.hkv) {
+        g = 0;
+        i0 += 2 * p.T;
+        while (i0 >= s.ql) {
+          if (s.b + 1 >= p.B) {  // only if the lengths change under the call
+            left = 0;
+            return false;
+          }
+          paged_seq(p, s.b + 1, &s);
+          i0 = 0;
+        }
+        item(p);
+      }
+    }
+    first = off;
+    count = (int)min((long long)(k.n - off), left);
+    off += count;
+    left -= count;
+    return true;
+  }
+  __device__ __forceinline__ bool pair(const PagedAttnParams& p) const { return nt > p.T; }
+};
+
+namespace tc {
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// mbar_wait that also gives up once another role has (and says so to the others).
+__device__ __forceinline__ bool mbar_wait_or(uint64_t* bar, uint32_t parity,
+                                             volatile int32_t* gave_up) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*gave_up) return false;
+    if (global_ns() - t0 > 2000000000ull) {
+      *gave_up = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// Descriptor of an operand whose contiguous axis is not the contraction (V: 64 channels of
+// one key per 128-byte row, swizzled): groups of 8 keys are 1024 B apart, chunks of 64
+// channels PA_CHUNK.
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)(PA_CHUNK >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// kind::f16 with both operands of type T (fp32 result); bt: B's contiguous axis is N.
+template <class T> __device__ constexpr uint32_t idesc16(int M, int N, bool bt);
+template <> __device__ constexpr uint32_t idesc16<bf16>(int M, int N, bool bt) {
+  return idesc_bf16(M, N) | (bt ? 1u << 16 : 0u);
+}
+template <> __device__ constexpr uint32_t idesc16<__half>(int M, int N, bool bt) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24) |
+         (bt ? 1u << 16 : 0u);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A holds two 16-bit values a column.
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+#define DG_R32(r)                                                                                \
+  "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "   \
+  "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+#define DG_OUT32(c, r)                                                                            \
+  c(r[0]), c(r[1]), c(r[2]), c(r[3]), c(r[4]), c(r[5]), c(r[6]), c(r[7]), c(r[8]), c(r[9]),      \
+      c(r[10]), c(r[11]), c(r[12]), c(r[13]), c(r[14]), c(r[15]), c(r[16]), c(r[17]), c(r[18]),  \
+      c(r[19]), c(r[20]), c(r[21]), c(r[22]), c(r[23]), c(r[24]), c(r[25]), c(r[26]), c(r[27]),  \
+      c(r[28]), c(r[29]), c(r[30]), c(r[31])
+
+// 32 columns of this warp's lanes; the registers hold them after tmem_wait32.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" DG_R32() "}, [%32];"
+               : DG_OUT32("=f", r)
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait32(float* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : DG_OUT32("+f", r)::"memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {" DG_R32() "};" ::DG_OUT32("r", r),
+               "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+#undef DG_R32
+#undef DG_OUT32
+
+}  // namespace tc
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<bf16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+struct PagedPlan {
+  long long total, skip;  // tiles of the line; tiles of sequence b before this CTA's part
+  int b;
+  int32_t gave_up;
+  long long sums[PA_THREADS / 32];
+  int32_t bad[4];  // a page out of range, by piece modulo 4
+};
+
+struct PagedBars {
+  uint64_t q_full, q_empty, done;
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t full[8], empty[8];
+};
+static_assert(sizeof(PagedPlan) + sizeof(PagedBars) <= 512, "fits the tail of shared memory");
+
+// Fills plan.total, and plan.b / plan.skip for the CTA that takes part `c` of `parts` (parts
+// follows from the total).  Every thread of the CTA calls it.
+__device__ __forceinline__ int paged_plan(const PagedAttnParams& p, PagedPlan* plan, int c) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long base = 0, mine = 0, incl = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long start = 0;
+    if (pass == 1) {
+      const int parts = (int)min((long long)PA_CTAS, (base + 1) / 2);
+      if (base == 0 || c >= parts) return parts;
+      start = base * c / parts;
+      if (tid == 0) plan->total = base;
+      base = 0;
+    }
+    for (int b0 = 0; b0 < p.B; b0 += PA_THREADS) {
+      const int b = b0 + tid;
+      if (pass == 0 || p.B > PA_THREADS) {  // up to one sequence a thread: once is enough
+        mine = 0;
+        if (b < p.B) {
+          PagedSeq s;
+          if (paged_seq(p, b, &s) && pass == 0 && c == 0 && p.err)
+            atomicOr(p.err, DG_PAGED_BAD_BATCH);
+          mine = paged_work(p, s);
+        }
+        incl = mine;
 #pragma unroll
-  for (int i = 0; i < D; ++i) op[i] = narrow<T>(o[i] * inv);
-  if (p.lse && lane == 0)
-    p.lse[(long long)t * p.hq + j] =
-        bad ? nan : l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        __syncthreads();
+        if (lane == 31) plan->sums[warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) incl += plan->sums[w];
+      }
+      long long all = 0;
+      for (int w = 0; w < PA_THREADS / 32; ++w) all += plan->sums[w];
+      if (pass == 1 && start >= base + incl - mine && start < base + incl) {
+        plan->b = b;
+        plan->skip = start - (base + incl - mine);
+      }
+      base += all;
+    }
+  }
+  return (int)min((long long)PA_CTAS, (base + 1) / 2);
+}
+
+template <int N> __device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+constexpr int PA_REGS_HIGH = 208, PA_REGS_LOW = 88;
+
+// Registers: 12 warps launch with 168 a thread (64,512 in all); the softmax warpgroups,
+// which hold 128 scores each, take 208 and leave the other four warps 88
+// (256 x 208 + 128 x 88 = 64,512).
+template <class T, int H>
+__global__ void __launch_bounds__(PA_THREADS, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const PagedAttnParams p) {
+  typedef PagedCfg<H> Cfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~(uintptr_t)1023);
+  uint8_t* sq = smem;                       // 2 row tiles
+  uint8_t* ring = sq + 2 * Cfg::TILE;       // SLOTS key or value tiles
+  PagedBars* bar = reinterpret_cast<PagedBars*>(ring + Cfg::SLOTS * Cfg::TILE);
+  PagedPlan* plan = reinterpret_cast<PagedPlan*>(bar + 1);
+  float2* xml = reinterpret_cast<float2*>(ring + Cfg::SLOTS * Cfg::TILE + 512);  // [2][128]
+  __shared__ uint32_t tslot;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    tc::mbar_init(&bar->q_full, 1);
+    tc::mbar_init(&bar->q_empty, 1);
+    tc::mbar_init(&bar->done, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar->s_full + i, 1);
+      tc::mbar_init(bar->p_full + i, 4);
+      tc::mbar_init(bar->o_full + i, 1);
+    }
+    for (int i = 0; i < Cfg::SLOTS; ++i) {
+      tc::mbar_init(bar->full + i, 1);
+      tc::mbar_init(bar->empty + i, 1);
+    }
+    tc::fence_mbar_init();
+    plan->gave_up = 0;
+    for (int i = 0; i < 4; ++i) plan->bad[i] = 0;
+  }
+  if (warp == 8) tc::tmem_alloc(&tslot, 512);
+  if (tid == PA_THREADS - 32) {
+    tc::prefetch_tmap(&mq);
+    tc::prefetch_tmap(&mk);
+    tc::prefetch_tmap(&mv);
+  }
+  pdl_enter();
+  const int c = blockIdx.x;
+  const int parts = paged_plan(p, plan, c);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tslot;
+  volatile int32_t* gave_up = &plan->gave_up;
+
+  if (tid == 0) p.rec[c].valid = 0;
+  const bool idle = c >= parts;
+  const long long total = idle ? 0 : plan->total;
+  PagedWalk w;
+  w.start(p, idle ? 0 : plan->b, idle ? 0 : plan->skip,
+          idle ? 0 : total * (c + 1) / parts - total * c / parts);
+  bool ok = true;
+
+  if (warp >= 8) {
+  reg_dec<PA_REGS_LOW>();
+  if (warp == 9) {
+    // ------------------------------------------------------------------ TMA
+    uint32_t n = 0, nq = 0, piece = 0;  // tiles and row tiles requested, pieces
+    const int rows = min(1 << p.page_log2, PA_KT), npg = PA_KT / rows;
+    auto load = [&](const CUtensorMap* map, int tile) {
+      const int s = n % Cfg::SLOTS;
+      ok = ok && tc::mbar_wait_or(bar->empty + s, ((n / Cfg::SLOTS) & 1) ^ 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const int pg = lane & (npg - 1);
+      const int key = tile * PA_KT + pg * rows;
+      const bool need = lane < npg * Cfg::CH && key < w.k.hi && key + rows > w.k.lo;
+      const int id = need ? p.table[(long long)w.s.b * p.max_pages + (key >> p.page_log2)] : -1;
+      const bool good = need && id >= 0 && id < p.n_pages;
+      const unsigned mask = __ballot_sync(0xffffffffu, good);
+      if (__any_sync(0xffffffffu, need && !good) && lane == 0) {
+        plan->bad[piece & 3] = 1;
+        if (p.err) atomicOr(p.err, DG_PAGED_BAD_PAGE);
+      }
+      if (lane == 0) tc::mbar_expect_tx(bar->full + s, __popc(mask) * rows * 128);
+      __syncwarp();
+      if (good) {
+        const int ch = lane / npg;
+        tc::tma_load_4d(ring + s * Cfg::TILE + ch * PA_CHUNK + pg * rows * 128, map, bar->full + s,
+                        ch * 64, key & ((1 << p.page_log2) - 1), w.g, id);
+      }
+      ++n;
+    };
+    for (; w.next(p); ++piece) {
+      const bool pair = w.pair(p);
+      ok = ok && tc::mbar_wait_or(&bar->q_empty, (piece & 1) ^ 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        const int tiles = pair ? 2 : 1;
+        ++nq;
+        if (lane == 0) {
+          plan->bad[piece & 3] = 0;
+          tc::mbar_expect_tx(&bar->q_full, tiles * Cfg::CH * p.G * p.T * 128);
+        }
+        __syncwarp();
+        if (lane < tiles * Cfg::CH) {
+          const int t = lane / Cfg::CH, ch = lane % Cfg::CH;
+          tc::tma_load_3d(sq + t * Cfg::TILE + ch * PA_CHUNK, &mq, &bar->q_full, ch * 64,
+                          w.g * p.G, w.s.q0 + w.i0 + t * p.T);
+        }
+      }
+      // in the order of first use (the MMA warp's loop)
+      const int t0 = w.k.t0 + w.first, steps = pair ? 2 * w.count : w.count;
+#pragma unroll 1
+      for (int u = -2; u < steps; ++u) {
+        if (pair && (u & 1)) continue;
+        if (u >= 0) load(&mv, t0 + (pair ? u >> 1 : u));
+        if (u + 2 < steps) load(&mk, t0 + (pair ? (u + 2) >> 1 : u + 2));
+      }
+    }
+    // no copy may land after the CTA has gone: normally all have been waited for already
+    if (!tc::drain_slots(bar->full, Cfg::SLOTS, (int)n)) *gave_up = 1;
+    if (nq > 0 && !tc::mbar_wait(&bar->q_full, (nq - 1) & 1)) *gave_up = 1;
+  } else if (warp == 8) {
+    // ------------------------------------------------------------------ MMA
+    uint32_t n = 0, piece = 0;      // tiles used, pieces
+    uint32_t pc = 0;                // parity of each stream's P tiles
+    constexpr uint32_t idS = tc::idesc16<T>(128, 128, false);
+    constexpr uint32_t idO = tc::idesc16<T>(128, H, true);
+    const uint64_t q_desc = tc::sdesc_k128(tc::smem_addr(sq));
+    const uint64_t k_desc = tc::sdesc_k128(tc::smem_addr(ring));
+    const uint64_t v_desc = tc::sdesc_mn128(tc::smem_addr(ring));
+    auto slot_wait = [&](uint32_t i) {
+      ok = ok && tc::mbar_wait_or(bar->full + i % Cfg::SLOTS, (i / Cfg::SLOTS) & 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::fence_after_sync();
+    };
+    // values nobody sees become 0, so that 0 * value is 0 whatever the slot held
+    auto clear_v = [&](uint32_t i, int tile) {
+      const int lo = min(max(w.k.lo - tile * PA_KT, 0), PA_KT);
+      const int hi = min(max(w.k.hi - tile * PA_KT, lo), PA_KT);
+      if (!ok || (lo == 0 && hi == PA_KT)) return;
+      uint8_t* v = ring + (i % Cfg::SLOTS) * Cfg::TILE;
+      for (int ch = 0; ch < Cfg::CH; ++ch) {
+        uint8_t* vc = v + ch * PA_CHUNK;
+        for (int x = lane; x < lo * 8; x += 32)
+          *reinterpret_cast<uint4*>(vc + x * 16) = make_uint4(0, 0, 0, 0);
+        for (int x = hi * 8 + lane; x < PA_KT * 8; x += 32)
+          *reinterpret_cast<uint4*>(vc + x * 16) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    };
+    for (; w.next(p); ++piece) {
+      const bool pair = w.pair(p);
+      const int t0 = w.k.t0 + w.first, steps = pair ? 2 * w.count : w.count;
+      ok = ok && tc::mbar_wait_or(&bar->q_full, piece & 1, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+      uint32_t v = 0, kk = 0;  // ring tiles in use
+      // Step u adds P V of stream u & 1 and issues the same stream's next scores, two steps
+      // ahead.  Solo: step u is key tile u.  Pair: steps 2 i and 2 i + 1 are key tile i.
+#pragma unroll 1
+      for (int u = -2; u < steps; ++u) {
+        const int t = u & 1;
+        if (u >= 0) {
+          if (!pair || t == 0) {
+            v = n++;
+            slot_wait(v);
+            clear_v(v, t0 + (pair ? u >> 1 : u));
+          }
+          ok = ok && tc::mbar_wait_or(bar->p_full + t, (pc >> t) & 1, gave_up);
+          ok = __all_sync(0xffffffffu, ok);
+          pc ^= 1u << t;
+          tc::fence_after_sync();
+          if (ok && lane == 0) {  // O_t += P_t V
+            const uint64_t vd = v_desc + (uint64_t)((v % Cfg::SLOTS) * (Cfg::TILE >> 4));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc::mma_ts(tmem + 256 + t * H, tmem + t * 128 + k * 8, vd + k * (2048 >> 4), idO,
+                         u >= 2 || k != 0);
+            if (u + 2 >= steps) tc::mma_commit(bar->o_full + t);
+            if (!pair || t == 1) tc::mma_commit(bar->empty + v % Cfg::SLOTS);
+          }
+          __syncwarp();
+        }
+        if (u + 2 < steps) {
+          if (!pair || t == 0) {
+            kk = n++;
+            slot_wait(kk);
+          }
+          if (ok && lane == 0) {  // S_t = Q K^T
+            const uint64_t qd = q_desc + (uint64_t)(pair && t ? Cfg::TILE >> 4 : 0);
+            const uint64_t kd = k_desc + (uint64_t)((kk % Cfg::SLOTS) * (Cfg::TILE >> 4));
+#pragma unroll
+            for (int k = 0; k < 4 * Cfg::CH; ++k) {
+              const uint32_t o = ((k >> 2) * PA_CHUNK + (k & 3) * 32) >> 4;
+              tc::mma_bf16(tmem + t * 128, qd + o, kd + o, idS, k != 0);
+            }
+            tc::mma_commit(bar->s_full + t);
+            if (!pair || t == 1) tc::mma_commit(bar->empty + kk % Cfg::SLOTS);
+            if (u + 3 == steps) tc::mma_commit(&bar->q_empty);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    // nothing of the tensor cores' may be in flight when TMEM is freed
+    if (lane == 0) {
+      tc::mma_commit(&bar->done);
+      if (!tc::mbar_wait(&bar->done, 0)) *gave_up = 1;
+    }
+  }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    reg_inc<PA_REGS_HIGH>();
+    const int t = warp >> 2, quarter = warp & 3;
+    const int r = 32 * quarter + lane;
+    const int tok = r / p.G, head = r - tok * p.G;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * H + lanes;
+    const float sl = p.scale_log2;
+    uint32_t sc = 0, oc = 0, piece = 0;
+    for (; w.next(p); ++piece) {
+      const bool pair = w.pair(p);
+      const int i0 = pair ? t * p.T : 0;  // first token of this row tile within the item
+      const int cnt = pair ? w.count : (w.count + 1 - t) >> 1;
+      const bool live = tok < p.T && i0 + tok < w.nt;
+      // keys this row sees; a row of no token takes any
+      int lo = 0, hi = 0x7fffffff;
+      if (live) {
+        const PagedKeys k1 = paged_keys(p, w.s, w.i0 + i0 + tok, 1);
+        lo = k1.lo;
+        hi = k1.hi;
+      }
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo);
+      const int hi_min = __reduce_min_sync(0xffffffffu, hi);
+      const bool work = __any_sync(0xffffffffu, live);
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < cnt; ++i) {
+        const int key0 = (w.k.t0 + w.first + (pair ? i : 2 * i + t)) * PA_KT;
+        ok = ok && tc::mbar_wait_or(bar->s_full + t, sc & 1, gave_up);
+        ++sc;
+        ok = __all_sync(0xffffffffu, ok);
+        if (work && ok) {
+          tc::fence_after_sync();
+          float s[128];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tc::tmem_ld32_async(ts + 32 * q, s + 32 * q);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tc::tmem_wait32(s + 32 * q);
+          if (key0 < lo_max || key0 + PA_KT > hi_min) {
+            const int a = lo - key0, z = hi - key0;
+#pragma unroll
+            for (int q = 0; q < 128; ++q) s[q] = q >= a && q < z ? s[q] : -INFINITY;
+          }
+          float mx[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = s[q];
+#pragma unroll
+          for (int q = 4; q < 128; ++q) mx[q & 3] = fmaxf(mx[q & 3], s[q]);
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+          const bool grow = mt > m + 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? mt : m;
+            const float a = grow ? ex2(m - mn) : 1.f;
+            l *= a;
+            m = mn;
+            if (i > 0) {
+#pragma unroll 1
+              for (int q = 0; q < H; q += 32) {
+                float o[32];
+                tc::tmem_ld32_async(to + q, o);
+                tc::tmem_wait32(o);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] *= a;
+                uint32_t ou[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) ou[x] = __float_as_uint(o[x]);
+                tc::tmem_st32(to + q, ou);
+              }
+            }
+          }
+          const float neg = m == -INFINITY ? 0.f : -m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              const float e0 = ex2(fmaf(s[64 * hf + 2 * q], sl, neg));
+              const float e1 = ex2(fmaf(s[64 * hf + 2 * q + 1], sl, neg));
+              sum[(2 * q) & 3] += e0;
+              sum[(2 * q + 1) & 3] += e1;
+              pk[q] = pack2<T>(e0, e1);
+            }
+            tc::tmem_st32(ts + 32 * hf, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc::tmem_wait_st();
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar->p_full + t);
+      }
+      if (cnt > 0) {
+        ok = ok && tc::mbar_wait_or(bar->o_full + t, oc & 1, gave_up);
+        ++oc;
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      // ---- the piece's rows: whole items to out, cut ones to the workspace
+      const bool bad = plan->bad[piece & 3] != 0;
+      const bool begins = w.first == 0, ends = w.off == w.k.n;
+      const long long grow_ = (long long)w.s.q0 + w.i0 + i0 + tok;
+      const int hq = w.g * p.G + head;
+      const long long prow = ((long long)c * 2 + (begins ? 1 : 0)) * p.part_rows +
+                             (pair ? t * 128 : 0) + r;
+      float w0 = 1.f, w1 = 0.f;  // weights of this stream's and the other's O
+      float M = m, L = l;
+      if (!pair) {
+        xml[t * 128 + r] = make_float2(m, l);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float2 a = xml[r], b = xml[128 + r];
+        M = fmaxf(a.x, b.x);
+        w0 = a.x == -INFINITY ? 0.f : ex2(a.x - M);
+        w1 = b.x == -INFINITY ? 0.f : ex2(b.x - M);
+        L = w0 * a.y + w1 * b.y;
+      }
+      if (bad) L = __int_as_float(0x7fc00000);
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const bool whole = begins && ends;
+      if (work && ok) {
+        tc::fence_after_sync();
+        const int c_lo = pair ? 0 : t * (H / 2), c_hi = pair ? H : c_lo + H / 2;
+        const bool two = !pair && w.count > 1;
+#pragma unroll 1
+        for (int q = c_lo; q < c_hi; q += 32) {
+          float o[32];
+          if (pair) {
+            tc::tmem_ld32_async(to + q, o);
+            tc::tmem_wait32(o);
+          } else {
+            tc::tmem_ld32_async(tmem + 256 + lanes + q, o);
+            tc::tmem_wait32(o);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = w0 == 0.f ? 0.f : o[x] * w0;
+            if (two) {
+              float o2[32];
+              tc::tmem_ld32_async(tmem + 256 + H + lanes + q, o2);
+              tc::tmem_wait32(o2);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] += w1 == 0.f ? 0.f : o2[x] * w1;
+            }
+          }
+          if (live && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
+                                                  (grow_ * p.hq + hq) * H + q);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              dst[x] = make_uint4(pack2<T>(o[8 * x] * inv, o[8 * x + 1] * inv),
+                                  pack2<T>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                                  pack2<T>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                                  pack2<T>(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
+          } else if (live) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * H + q);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+        }
+      }
+      if (live && (pair || t == 0)) {
+        if (!whole)
+          p.part_ml[prow] = make_float2(M, L);
+        else if (p.lse)
+          p.lse[grow_ * p.hq + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      }
+      if (!pair) {
+        // both warpgroups have read both accumulators and xml
+        tc::fence_before_sync();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+      if (tid == 0 && begins && !ends) {
+        // the line's position of the item's end gives the last CTA that holds a piece
+        const long long at = total * (c + 1) / parts - w.left - w.count + w.k.n;
+        PagedRec rec;
+        rec.valid = 1;
+        rec.last = (int)((at * parts - 1) / total);
+        rec.row0 = w.s.q0 + w.i0;
+        rec.ntok = w.nt;
+        rec.g = w.g;
+        p.rec[c] = rec;
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (tid == 0 && plan->gave_up && p.err) atomicOr(p.err, DG_PAGED_TIMEOUT);
+  if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+// Adds the pieces of cut items: block (c, y) takes rows y * PM_ROWS .. of the item that
+// starts and does not end in CTA c, a warp a row.
+constexpr int PM_WARPS = 8, PM_ROWS = 16;
+
+template <class T, int H>
+__global__ void __launch_bounds__(PM_WARPS * 32) paged_merge_kernel(const PagedAttnParams p) {
+  pdl_enter();
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const PagedRec rec = p.rec[c];
+  if (!rec.valid) return;
+  constexpr int D = H / 32;
+  for (int i = warp; i < PM_ROWS; i += PM_WARPS) {
+    const int row = blockIdx.y * PM_ROWS + i;  // row tile * 128 + row
+    if (row >= p.part_rows) break;
+    const int r = row & 127, tk = r / p.G, tok = (row >> 7) * p.T + tk;
+    if (tk >= p.T || tok >= rec.ntok) continue;
+    auto piece = [&](int k) {  // k-th piece's row
+      return ((long long)(c + k) * 2 + (k == 0 ? 1 : 0)) * p.part_rows + row;
+    };
+    const int n = rec.last - c + 1;
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[piece(k)].x);
+    M = warp_max(M);
+    float o[D], L = 0.f;
+#pragma unroll
+    for (int x = 0; x < D; ++x) o[x] = 0.f;
+    for (int k = 0; k < n; ++k) {
+      const float2 ml = p.part_ml[piece(k)];
+      const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+      L += ml.y != ml.y ? ml.y : wt * ml.y;  // NaN: a page out of range
+      const float* src = p.part_o + piece(k) * H + D * lane;
+#pragma unroll
+      for (int x = 0; x < D; ++x) o[x] += wt == 0.f ? 0.f : wt * src[x];
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const long long at = ((long long)(rec.row0 + tok) * p.hq + rec.g * p.G + r % p.G);
+    T* dst = static_cast<T*>(p.out) + at * H + D * lane;
+#pragma unroll
+    for (int x = 0; x < D; x += 2)
+      *reinterpret_cast<uint32_t*>(dst + x) = pack2<T>(o[x] * inv, o[x + 1] * inv);
+    if (p.lse && lane == 0)
+      p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
 }
 
 }  // namespace dg

@@ -1,4 +1,7 @@
 // Host side of the paged-cache operators (include/dg_paged.h): argument checks and launches.
+#include <cudaTypedefs.h>
+
+#include <atomic>
 #include <cmath>
 
 #include "dg_internal.h"
@@ -152,6 +155,76 @@ dg_status launch_rows(RowsParams& p, const dg_rope* rope, cudaStream_t st, const
                        what);
 }
 
+// The tensor-map encoder, looked up once (the same for every device).
+dg_status encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
+  static std::atomic<void*> found{nullptr};
+  void* fn = found.load(std::memory_order_acquire);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e =
+        cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
+    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) {
+      set_error("cuTensorMapEncodeTiled entry point unavailable");
+      return DG_ERR_CUDA;
+    }
+    found.store(fn, std::memory_order_release);
+  }
+  *out = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  return DG_OK;
+}
+
+// 16-bit tensor of `rank` dimensions (strides in elements, of dimensions 1 on), 128-byte
+// swizzled boxes of 64 channels, zero outside.  An axis of one element has any stride.
+dg_status encode(PFN_cuTensorMapEncodeTiled_v12000 enc, int dtype, const void* p, int rank,
+                 const cuuint64_t* dims, const long long* strides, const cuuint32_t* box,
+                 CUtensorMap* m) {
+  cuuint64_t st[3];
+  for (int i = 0; i + 1 < rank; ++i) st[i] = (dims[i + 1] == 1 ? dims[0] : strides[i]) * 2;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  const CUresult r = enc(
+      m, dtype == DG_ELEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+      rank, const_cast<void*>(p), dims, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return DG_ERR_CUDA;
+  }
+  return DG_OK;
+}
+
+// Rows of a piece: the tokens of an item (two row tiles, or one with at most max_q) times
+// the heads of a group.
+int piece_rows(const dg_paged_batch* b, int group) {
+  const int T = 128 / group;
+  return b->max_q > T ? 256 : b->max_q * group;
+}
+
+size_t attention_bytes(const dg_paged_batch* b, int group, int h) {
+  return PA_CTAS * (sizeof(PagedRec) + 2 * (size_t)piece_rows(b, group) * (h + 2) * 4) + 256;
+}
+
+template <class T, int H>
+dg_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                           const PagedAttnParams& p, cudaStream_t st) {
+  static std::atomic<bool> ready[64];  // per device: the kernel's shared-memory limit is set
+  int dev = 0;
+  DG_TRY_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    DG_TRY_CUDA(cudaFuncSetAttribute(paged_attn_kernel<T, H>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)PagedCfg<H>::SMEM));
+    if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  DG_TRY(launch_status(launch_pdl(paged_attn_kernel<T, H>, dim3(PA_CTAS), dim3(PA_THREADS),
+                                  PagedCfg<H>::SMEM, st, 1, mq, mk, mv, p),
+                       "dg_paged_attention"));
+  return launch_status(
+      launch_pdl(paged_merge_kernel<T, H>, dim3(PA_CTAS, (p.part_rows + PM_ROWS - 1) / PM_ROWS),
+                 dim3(PM_WARPS * 32), 0, st, 1, p),
+      "dg_paged_attention (merge)");
+}
+
 }  // namespace
 
 extern "C" {
@@ -286,7 +359,8 @@ dg_status dg_paged_attention_workspace(const dg_paged_cache* cache, const dg_pag
   DG_TRY(check_batch(cache, batch));
   DG_REQUIRE(n_q_heads >= 1 && n_q_heads % cache->n_kv_heads == 0,
              "n_q_heads=%d is no multiple of n_kv_heads=%d", n_q_heads, cache->n_kv_heads);
-  *bytes = 256;
+  const int group = n_q_heads / cache->n_kv_heads;
+  *bytes = group <= 128 ? attention_bytes(batch, group, cache->head_dim) : 0;
   return DG_OK;
 }
 
@@ -318,13 +392,31 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
   DG_TRY(dg_paged_attention_workspace(cache, batch, q->n_heads, &need));
   DG_REQUIRE(workspace && aligned(workspace, 256) && workspace_bytes >= need,
              "workspace must be 256-byte aligned and hold %zu bytes", need);
-  if (n == 0 || batch->B == 0) return DG_OK;
+  // the tensor maps that describe q cannot repeat or overlap rows
+  DG_REQUIRE((n <= 1 || q->token_stride >= 8) && (q->n_heads == 1 || q->head_stride >= 8),
+             "q: strides of 0");
+  if (n == 0 || batch->B == 0 || batch->max_q == 0) return DG_OK;
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  DG_TRY(encoder(&enc));
   PagedAttnParams p{};
-  p.k = static_cast<const char*>(cache->k);
-  p.v = static_cast<const char*>(cache->v);
-  p.ps = cache->page_stride * 2;
-  p.ts = cache->token_stride * 2;
-  p.hs = cache->head_stride * 2;
+  p.G = group;
+  p.T = 128 / group;
+  CUtensorMap mq, mk, mv;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)h, (cuuint64_t)q->n_heads, (cuuint64_t)n};
+    const long long str[2] = {q->head_stride, q->token_stride};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.T};
+    DG_TRY(encode(enc, cache->dtype, q->p, 3, dims, str, box, &mq));
+  }
+  {
+    const cuuint64_t dims[4] = {(cuuint64_t)h, (cuuint64_t)cache->page_size,
+                                (cuuint64_t)cache->n_kv_heads, (cuuint64_t)cache->n_pages};
+    const long long str[3] = {cache->token_stride, cache->head_stride, cache->page_stride};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(cache->page_size < PA_KT ? cache->page_size : PA_KT),
+                               1, 1};
+    DG_TRY(encode(enc, cache->dtype, cache->k, 4, dims, str, box, &mk));
+    DG_TRY(encode(enc, cache->dtype, cache->v, 4, dims, str, box, &mv));
+  }
   p.page_log2 = ilog2(cache->page_size);
   p.n_pages = cache->n_pages;
   p.max_pages = batch->max_pages;
@@ -334,7 +426,6 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
   p.q_start = batch->q_start;
   p.kv_len = batch->kv_len;
   p.table = batch->page_table;
-  p.q = heads_dev(q, 2);
   p.hq = q->n_heads;
   p.hkv = cache->n_kv_heads;
   p.causal = causal;
@@ -344,17 +435,18 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
   p.out = out;
   p.lse = lse;
   p.err = err;
+  p.part_rows = piece_rows(batch, group);
+  char* ws = static_cast<char*>(workspace);
+  const size_t rows = (size_t)PA_CTAS * 2 * p.part_rows;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + rows * h * 4);
+  p.rec = reinterpret_cast<PagedRec*>(ws + rows * h * 4 + rows * 8);
   cudaStream_t st = (cudaStream_t)stream;
-  const long long blocks = ((long long)n * p.hq + 7) / 8;
-  DG_REQUIRE(blocks <= 0x7fffffffLL, "too many rows");
-#define DG_PAGED_ROWS(T, H)                                                                  \
-  launch_status(launch_pdl(paged_attn_rows_kernel<T, H>, dim3((unsigned)blocks), dim3(256), 0, \
-                           st, 1, p),                                                        \
-                "dg_paged_attention")
   if (cache->dtype == DG_ELEM_BF16)
-    return h == 64 ? DG_PAGED_ROWS(bf16, 64) : DG_PAGED_ROWS(bf16, 128);
-  return h == 64 ? DG_PAGED_ROWS(__half, 64) : DG_PAGED_ROWS(__half, 128);
-#undef DG_PAGED_ROWS
+    return h == 64 ? launch_attention<bf16, 64>(mq, mk, mv, p, st)
+                   : launch_attention<bf16, 128>(mq, mk, mv, p, st);
+  return h == 64 ? launch_attention<__half, 64>(mq, mk, mv, p, st)
+                 : launch_attention<__half, 128>(mq, mk, mv, p, st);
 }
 
 }  // extern "C"
