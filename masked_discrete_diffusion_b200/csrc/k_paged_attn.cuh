@@ -12,8 +12,9 @@
 // meet at the end.  Either way two softmax warpgroups work while the tensor cores fill the
 // other's scores.
 //
-// Split.  All items' key tiles form one line; 148 CTAs take equal contiguous parts of it, so
-// no length mix leaves SMs idle.  A CTA's part is a run of whole items with a cut one at
+// Split.  All items form one line, each as long as its key tiles plus PA_ITEM (what filling
+// and emptying the pipeline for it costs, in tiles); 148 CTAs take equal contiguous parts of
+// it, so no length mix leaves SMs idle.  A CTA's part is a run of whole items with a cut one at
 // either end; cut pieces leave (m, l, O) in the workspace and paged_merge_kernel adds an
 // item's pieces in the order of the line (the same bits every time).  Each CTA finds its
 // part from the lengths on the device: no host plan, and a captured graph follows them.
@@ -34,6 +35,7 @@ namespace dg {
 constexpr int PA_CTAS = 148;
 constexpr int PA_THREADS = 384;  // 12 warps: 8 softmax, MMA, TMA, 2 that only help to plan
 constexpr int PA_KT = 128;                 // keys a tile
+constexpr int PA_ITEM = 2;                 // an item's fixed cost in tiles
 constexpr uint32_t PA_CHUNK = 128 * 128;   // 128 rows of 64 channels
 
 template <int H> struct PagedCfg {
@@ -41,7 +43,8 @@ template <int H> struct PagedCfg {
   static constexpr uint32_t TILE = CH * PA_CHUNK;   // a Q, K or V tile
   static constexpr int SLOTS = H == 128 ? 4 : 8;
   static constexpr size_t SMEM =
-      1024 + (2 + SLOTS) * TILE + 512 /* barriers, plan */ + 2 * 128 * 8 /* m, l */;
+      1024 + (2 + SLOTS) * TILE + 512 /* barriers, plan */ + 2 * 128 * 8 /* m, l */ +
+      8 * 2048 /* output staging */;
 };
 
 struct PagedAttnParams {
@@ -57,7 +60,7 @@ struct PagedAttnParams {
   int32_t* err;
   // workspace
   int part_rows;  // rows of a piece
-  float* part_o;  // [PA_CTAS][2][part_rows][H]
+  float4* part_o;   // [PA_CTAS][2][H / 4][part_rows]: a warp's rows are contiguous
   float2* part_ml;  // [PA_CTAS][2][part_rows]
   struct PagedRec* rec;  // [PA_CTAS]
 };
@@ -113,7 +116,7 @@ __device__ __forceinline__ PagedKeys paged_keys(const PagedAttnParams& p, const 
 __device__ __forceinline__ long long paged_work(const PagedAttnParams& p, const PagedSeq& s) {
   long long w = 0;
   for (int i0 = 0; i0 < s.ql; i0 += 2 * p.T)
-    w += paged_keys(p, s, i0, min(2 * p.T, s.ql - i0)).n;
+    w += paged_keys(p, s, i0, min(2 * p.T, s.ql - i0)).n + PA_ITEM;
   return w * p.hkv;
 }
 
@@ -123,9 +126,9 @@ struct PagedWalk {
   PagedKeys k;
   int i0, nt;    // the item's tokens
   int g;         // its key head
-  int off;       // tiles of it that lie before
+  int off;       // line units of it that lie before
   long long left;
-  // the current piece
+  // the current piece: key tiles first .. first + count - 1 of the item
   int first, count;
 
   __device__ __forceinline__ void item(const PagedAttnParams& p) {
@@ -139,38 +142,41 @@ struct PagedWalk {
     paged_seq(p, b, &s);
     i0 = 0;
     item(p);
-    while (skip >= (long long)k.n * p.hkv && i0 + 2 * p.T < s.ql) {
-      skip -= (long long)k.n * p.hkv;
+    while (skip >= (long long)(k.n + PA_ITEM) * p.hkv && i0 + 2 * p.T < s.ql) {
+      skip -= (long long)(k.n + PA_ITEM) * p.hkv;
       i0 += 2 * p.T;
       item(p);
     }
-    g = (int)(skip / k.n);
-    off = (int)(skip % k.n);
+    g = (int)(skip / (k.n + PA_ITEM));
+    off = (int)(skip % (k.n + PA_ITEM));
   }
   // Prepares the next piece; false at the end of the part.
   __device__ __forceinline__ bool next(const PagedAttnParams& p) {
-    if (left <= 0) return false;
-    if (off == k.n) {  // the item is done: next head, tokens, sequence
-      off = 0;
-      if (++g == p.hkv) {
-        g = 0;
-        i0 += 2 * p.T;
-        while (i0 >= s.ql) {
-          if (s.b + 1 >= p.B) {  // only if the lengths change under the call
-            left = 0;
-            return false;
+    while (left > 0) {
+      if (off == k.n + PA_ITEM) {  // the item is done: next head, tokens, sequence
+        off = 0;
+        if (++g == p.hkv) {
+          g = 0;
+          i0 += 2 * p.T;
+          while (i0 >= s.ql) {
+            if (s.b + 1 >= p.B) {  // only if the lengths change under the call
+              left = 0;
+              return false;
+            }
+            paged_seq(p, s.b + 1, &s);
+            i0 = 0;
           }
-          paged_seq(p, s.b + 1, &s);
-          i0 = 0;
+          item(p);
         }
-        item(p);
       }
+      const int take = (int)min((long long)(k.n + PA_ITEM - off), left);
+      first = max(off - PA_ITEM, 0);
+      off += take;
+      left -= take;
+      count = max(off - PA_ITEM, 0) - first;
+      if (count > 0) return true;  // else the part ends within the item's fixed cost
     }
-    first = off;
-    count = (int)min((long long)(k.n - off), left);
-    off += count;
-    left -= count;
-    return true;
+    return false;
   }
   __device__ __forceinline__ bool pair(const PagedAttnParams& p) const { return nt > p.T; }
 };
@@ -284,6 +290,32 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two fp32 values in a register pair, for the packed instructions.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2<bf16>(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -304,10 +336,15 @@ struct PagedPlan {
 
 struct PagedBars {
   uint64_t q_full, q_empty, done;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[4] /* [stream][keys 0-63, 64-127] */, o_full[2];
   uint64_t full[8], empty[8];
 };
 static_assert(sizeof(PagedPlan) + sizeof(PagedBars) <= 512, "fits the tail of shared memory");
+
+// CTAs that share a line of this length: as many as leave each a tile beyond the fixed cost.
+__device__ __forceinline__ int paged_parts(long long total) {
+  return (int)min((long long)PA_CTAS, (total + PA_ITEM) / (PA_ITEM + 1));
+}
 
 // Fills plan.total, and plan.b / plan.skip for the CTA that takes part `c` of `parts` (parts
 // follows from the total).  Every thread of the CTA calls it.
@@ -317,7 +354,7 @@ __device__ __forceinline__ int paged_plan(const PagedAttnParams& p, PagedPlan* p
   for (int pass = 0; pass < 2; ++pass) {
     long long start = 0;
     if (pass == 1) {
-      const int parts = (int)min((long long)PA_CTAS, (base + 1) / 2);
+      const int parts = paged_parts(base);
       if (base == 0 || c >= parts) return parts;
       start = base * c / parts;
       if (tid == 0) plan->total = base;
@@ -353,7 +390,7 @@ __device__ __forceinline__ int paged_plan(const PagedAttnParams& p, PagedPlan* p
       base += all;
     }
   }
-  return (int)min((long long)PA_CTAS, (base + 1) / 2);
+  return paged_parts(base);
 }
 
 template <int N> __device__ __forceinline__ void reg_inc() {
@@ -381,6 +418,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   PagedBars* bar = reinterpret_cast<PagedBars*>(ring + Cfg::SLOTS * Cfg::TILE);
   PagedPlan* plan = reinterpret_cast<PagedPlan*>(bar + 1);
   float2* xml = reinterpret_cast<float2*>(ring + Cfg::SLOTS * Cfg::TILE + 512);  // [2][128]
+  uint4* stage = reinterpret_cast<uint4*>(xml + 256) + (threadIdx.x >> 5) * 128;  // 2 KB a warp
   __shared__ uint32_t tslot;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -390,7 +428,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     tc::mbar_init(&bar->done, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar->s_full + i, 1);
-      tc::mbar_init(bar->p_full + i, 4);
+      tc::mbar_init(bar->p_full + 2 * i, 4);
+      tc::mbar_init(bar->p_full + 2 * i + 1, 4);
       tc::mbar_init(bar->o_full + i, 1);
     }
     for (int i = 0; i < Cfg::SLOTS; ++i) {
@@ -531,16 +570,21 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             slot_wait(v);
             clear_v(v, t0 + (pair ? u >> 1 : u));
           }
-          ok = ok && tc::mbar_wait_or(bar->p_full + t, (pc >> t) & 1, gave_up);
-          ok = __all_sync(0xffffffffu, ok);
-          pc ^= 1u << t;
-          tc::fence_after_sync();
-          if (ok && lane == 0) {  // O_t += P_t V
-            const uint64_t vd = v_desc + (uint64_t)((v % Cfg::SLOTS) * (Cfg::TILE >> 4));
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc::mma_ts(tmem + 256 + t * H, tmem + t * 128 + k * 8, vd + k * (2048 >> 4), idO,
-                         u >= 2 || k != 0);
+          for (int hf = 0; hf < 2; ++hf) {  // O_t += P_t V, 64 keys at a time
+            ok = ok && tc::mbar_wait_or(bar->p_full + 2 * t + hf, (pc >> t) & 1, gave_up);
+            ok = __all_sync(0xffffffffu, ok);
+            tc::fence_after_sync();
+            if (ok && lane == 0) {
+              const uint64_t vd = v_desc + (uint64_t)((v % Cfg::SLOTS) * (Cfg::TILE >> 4));
+#pragma unroll
+              for (int k = 4 * hf; k < 4 * hf + 4; ++k)
+                tc::mma_ts(tmem + 256 + t * H, tmem + t * 128 + k * 8, vd + k * (2048 >> 4), idO,
+                           u >= 2 || k != 0);
+            }
+          }
+          pc ^= 1u << t;
+          if (ok && lane == 0) {
             if (u + 2 >= steps) tc::mma_commit(bar->o_full + t);
             if (!pair || t == 1) tc::mma_commit(bar->empty + v % Cfg::SLOTS);
           }
@@ -607,21 +651,25 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (work && ok) {
           tc::fence_after_sync();
           float s[128];
+          const bool edge = key0 < lo_max || key0 + PA_KT > hi_min;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tc::tmem_ld32_async(ts, s);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tc::tmem_ld32_async(ts + 32 * q, s + 32 * q);
+          for (int q = 0; q < 4; ++q) {  // the next 32 scores arrive while these are compared
+            tc::tmem_wait32(s + 32 * q);
+            if (q < 3) tc::tmem_ld32_async(ts + 32 * (q + 1), s + 32 * (q + 1));
+            if (edge) {
+              const int a = lo - key0, z = hi - key0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tc::tmem_wait32(s + 32 * q);
-          if (key0 < lo_max || key0 + PA_KT > hi_min) {
-            const int a = lo - key0, z = hi - key0;
+              for (int x = 32 * q; x < 32 * q + 32; ++x) s[x] = x >= a && x < z ? s[x] : -INFINITY;
+            }
 #pragma unroll
-            for (int q = 0; q < 128; ++q) s[q] = q >= a && q < z ? s[q] : -INFINITY;
+            for (int x = 0; x < 32; x += 8)
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                mx[y] = max3(mx[y], s[32 * q + x + 2 * y], s[32 * q + x + 2 * y + 1]);
           }
-          float mx[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = s[q];
-#pragma unroll
-          for (int q = 4; q < 128; ++q) mx[q & 3] = fmaxf(mx[q & 3], s[q]);
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+          const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl;
           const bool grow = mt > m + 8.f;
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? mt : m;
@@ -634,36 +682,47 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 float o[32];
                 tc::tmem_ld32_async(to + q, o);
                 tc::tmem_wait32(o);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] *= a;
                 uint32_t ou[32];
 #pragma unroll
-                for (int x = 0; x < 32; ++x) ou[x] = __float_as_uint(o[x]);
+                for (int x = 0; x < 32; ++x) ou[x] = __float_as_uint(o[x] * a);
                 tc::tmem_st32(to + q, ou);
               }
             }
           }
           const float neg = m == -INFINITY ? 0.f : -m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sl2 = f2(sl, sl), neg2 = f2(neg, neg);
+          uint64_t sum2[2] = {0, 0};
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t pk[32];
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
-              const float e0 = ex2(fmaf(s[64 * hf + 2 * q], sl, neg));
-              const float e1 = ex2(fmaf(s[64 * hf + 2 * q + 1], sl, neg));
-              sum[(2 * q) & 3] += e0;
-              sum[(2 * q + 1) & 3] += e1;
+              float e0, e1;
+              unf2(fma2(f2(s[64 * hf + 2 * q], s[64 * hf + 2 * q + 1]), sl2, neg2), &e0, &e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum2[q & 1] = add2(sum2[q & 1], f2(e0, e1));
               pk[q] = pack2<T>(e0, e1);
             }
             tc::tmem_st32(ts + 32 * hf, pk);
+            tc::tmem_wait_st();
+            if (hf == 0) {  // P V starts on the first 64 keys
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
+            }
           }
+          float sum[4];
+          unf2(sum2[0], sum, sum + 1);
+          unf2(sum2[1], sum + 2, sum + 3);
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tc::tmem_wait_st();
+        } else {
+          tc::fence_before_sync();
+          if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar->p_full + t);
+        if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t + 1);
       }
       if (cnt > 0) {
         ok = ok && tc::mbar_wait_or(bar->o_full + t, oc & 1, gave_up);
@@ -672,11 +731,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       // ---- the piece's rows: whole items to out, cut ones to the workspace
       const bool bad = plan->bad[piece & 3] != 0;
-      const bool begins = w.first == 0, ends = w.off == w.k.n;
-      const long long grow_ = (long long)w.s.q0 + w.i0 + i0 + tok;
-      const int hq = w.g * p.G + head;
-      const long long prow = ((long long)c * 2 + (begins ? 1 : 0)) * p.part_rows +
-                             (pair ? t * 128 : 0) + r;
+      const bool begins = w.first == 0, ends = w.first + w.count == w.k.n;
+      // this row in out (-1: none), and in the workspace
+      const long long row_at =
+          live ? ((long long)w.s.q0 + w.i0 + i0 + tok) * p.hq + w.g * p.G + head : -1;
+      const long long piece_at = (long long)c * 2 + (begins ? 1 : 0);
+      const int piece_row = (pair ? t * 128 : 0) + r;
       float w0 = 1.f, w1 = 0.f;  // weights of this stream's and the other's O
       float M = m, L = l;
       if (!pair) {
@@ -714,28 +774,40 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
               for (int x = 0; x < 32; ++x) o[x] += w1 == 0.f ? 0.f : o2[x] * w1;
             }
           }
-          if (live && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
-                                                  (grow_ * p.hq + hq) * H + q);
+          if (whole) {
+            // through this warp's 2 KB of shared memory, so that a store instruction
+            // writes 64 contiguous bytes of 8 rows (chunks of 16 bytes, swizzled by row)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              dst[x] = make_uint4(pack2<T>(o[8 * x] * inv, o[8 * x + 1] * inv),
-                                  pack2<T>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
-                                  pack2<T>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
-                                  pack2<T>(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
+              stage[lane * 4 + (x ^ ((lane >> 1) & 3))] =
+                  make_uint4(pack2<T>(o[8 * x] * inv, o[8 * x + 1] * inv),
+                             pack2<T>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                             pack2<T>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                             pack2<T>(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int rr = 8 * x + (lane >> 2);
+              const uint4 v = stage[rr * 4 + ((lane & 3) ^ ((rr >> 1) & 3))];
+              const long long at = __shfl_sync(0xffffffffu, row_at, rr);
+              if (at >= 0)
+                reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * H + q)[lane & 3] = v;
+            }
+            __syncwarp();
           } else if (live) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * H + q);
+            float4* dst = p.part_o + (piece_at * (H / 4) + q / 4) * p.part_rows + piece_row;
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-              dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+              dst[x * (long long)p.part_rows] =
+                  make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           }
         }
       }
       if (live && (pair || t == 0)) {
         if (!whole)
-          p.part_ml[prow] = make_float2(M, L);
+          p.part_ml[piece_at * p.part_rows + piece_row] = make_float2(M, L);
         else if (p.lse)
-          p.lse[grow_ * p.hq + hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          p.lse[row_at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
       }
       if (!pair) {
         // both warpgroups have read both accumulators and xml
@@ -744,7 +816,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       if (tid == 0 && begins && !ends) {
         // the line's position of the item's end gives the last CTA that holds a piece
-        const long long at = total * (c + 1) / parts - w.left - w.count + w.k.n;
+        const long long at = total * (c + 1) / parts - w.left - w.off + w.k.n + PA_ITEM;
         PagedRec rec;
         rec.valid = 1;
         rec.last = (int)((at * parts - 1) / total);
@@ -762,48 +834,66 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 }
 
 // Adds the pieces of cut items: block (c, y) takes rows y * PM_ROWS .. of the item that
-// starts and does not end in CTA c, a warp a row.
-constexpr int PM_WARPS = 8, PM_ROWS = 16;
+// starts and does not end in CTA c.  Thread (row, 4 channels), rows fastest: a piece's
+// channels of 8 rows are one 128-byte line.
+constexpr int PM_ROWS = 8;
 
 template <class T, int H>
-__global__ void __launch_bounds__(PM_WARPS * 32) paged_merge_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(PM_ROWS * H / 4) paged_merge_kernel(const PagedAttnParams p) {
+  __shared__ float wts[PM_ROWS][PA_CTAS];
+  __shared__ float sums[PM_ROWS];
   pdl_enter();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int WARPS = PM_ROWS * H / 128;
   const PagedRec rec = p.rec[c];
   if (!rec.valid) return;
-  constexpr int D = H / 32;
-  for (int i = warp; i < PM_ROWS; i += PM_WARPS) {
-    const int row = blockIdx.y * PM_ROWS + i;  // row tile * 128 + row
+  const int n = min(rec.last, PA_CTAS - 1) - c + 1;
+  const int row0 = blockIdx.y * PM_ROWS;
+  // k-th piece: slot 1 of CTA c, then slot 0 of c + k
+  for (int i = warp; i < PM_ROWS; i += WARPS) {
+    const int row = row0 + i;
     if (row >= p.part_rows) break;
-    const int r = row & 127, tk = r / p.G, tok = (row >> 7) * p.T + tk;
-    if (tk >= p.T || tok >= rec.ntok) continue;
-    auto piece = [&](int k) {  // k-th piece's row
-      return ((long long)(c + k) * 2 + (k == 0 ? 1 : 0)) * p.part_rows + row;
-    };
-    const int n = rec.last - c + 1;
     float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[piece(k)].x);
+    for (int k = lane; k < n; k += 32)
+      M = fmaxf(M, p.part_ml[((long long)(c + k) * 2 + (k == 0)) * p.part_rows + row].x);
     M = warp_max(M);
-    float o[D], L = 0.f;
-#pragma unroll
-    for (int x = 0; x < D; ++x) o[x] = 0.f;
-    for (int k = 0; k < n; ++k) {
-      const float2 ml = p.part_ml[piece(k)];
+    float L = 0.f;
+    for (int k = lane; k < n; k += 32) {
+      const float2 ml = p.part_ml[((long long)(c + k) * 2 + (k == 0)) * p.part_rows + row];
       const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+      wts[i][k] = wt;
       L += ml.y != ml.y ? ml.y : wt * ml.y;  // NaN: a page out of range
-      const float* src = p.part_o + piece(k) * H + D * lane;
-#pragma unroll
-      for (int x = 0; x < D; ++x) o[x] += wt == 0.f ? 0.f : wt * src[x];
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const long long at = ((long long)(rec.row0 + tok) * p.hq + rec.g * p.G + r % p.G);
-    T* dst = static_cast<T*>(p.out) + at * H + D * lane;
-#pragma unroll
-    for (int x = 0; x < D; x += 2)
-      *reinterpret_cast<uint32_t*>(dst + x) = pack2<T>(o[x] * inv, o[x + 1] * inv);
-    if (p.lse && lane == 0)
-      p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    L = warp_sum(L);
+    if (lane == 0) {
+      sums[i] = L == 0.f ? 0.f : 1.f / L;
+      const int r = row & 127, tk = r / p.G, tok = (row >> 7) * p.T + tk;
+      if (p.lse && tk < p.T && tok < rec.ntok)
+        p.lse[(long long)(rec.row0 + tok) * p.hq + rec.g * p.G + r % p.G] =
+            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
   }
+  __syncthreads();
+  const int i = threadIdx.x % PM_ROWS, q = threadIdx.x / PM_ROWS, row = row0 + i;
+  const int r = row & 127, tk = r / p.G, tok = (row >> 7) * p.T + tk;
+  if (row >= p.part_rows || tk >= p.T || tok >= rec.ntok) return;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float4 v =
+        p.part_o[(((long long)(c + k) * 2 + (k == 0)) * (H / 4) + q) * p.part_rows + row];
+    const float wt = wts[i][k];
+    if (wt != 0.f) {
+      o.x += wt * v.x;
+      o.y += wt * v.y;
+      o.z += wt * v.z;
+      o.w += wt * v.w;
+    }
+  }
+  const float inv = sums[i];
+  const long long at = (long long)(rec.row0 + tok) * p.hq + rec.g * p.G + r % p.G;
+  *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * H + 4 * q) =
+      make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
 }
 
 }  // namespace dg

@@ -221,7 +221,7 @@ dg_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const C
                        "dg_paged_attention"));
   return launch_status(
       launch_pdl(paged_merge_kernel<T, H>, dim3(PA_CTAS, (p.part_rows + PM_ROWS - 1) / PM_ROWS),
-                 dim3(PM_WARPS * 32), 0, st, 1, p),
+                 dim3(PM_ROWS * H / 4), 0, st, 1, p),
       "dg_paged_attention (merge)");
 }
 
@@ -438,7 +438,7 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
   p.part_rows = piece_rows(batch, group);
   char* ws = static_cast<char*>(workspace);
   const size_t rows = (size_t)PA_CTAS * 2 * p.part_rows;
-  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_o = reinterpret_cast<float4*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + rows * h * 4);
   p.rec = reinterpret_cast<PagedRec*>(ws + rows * h * 4 + rows * 8);
   cudaStream_t st = (cudaStream_t)stream;
