@@ -20,7 +20,9 @@
 // part from the lengths on the device: no host plan, and a captured graph follows them.
 //
 // CTA.  Warps 0-3 and 4-7: the streams' softmax, a thread a row (TMEM lane = row).  Warp 8:
-// MMA issue.  Warp 9: TMA.  S (128 columns) and O of both streams fill TMEM; P takes S's
+// MMA issue for both streams in turn, which keeps one's softmax under the other's products
+// (with a warp for each the streams fell into step, 5,100 cycles a pair of tiles).
+// Warp 9: TMA.  S (128 columns) and O of both streams fill TMEM; P takes S's
 // place as the A operand of O += P V.  K and V tiles pass through one ring of slots in the
 // order of their first use.  O is rescaled only when a row's maximum has grown by 2^8, by
 // its own warp; until then P's exponents are taken against the older maximum, which the
@@ -240,6 +242,20 @@ template <> __device__ constexpr uint32_t idesc16<bf16>(int M, int N, bool bt) {
 template <> __device__ constexpr uint32_t idesc16<__half>(int M, int N, bool bt) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24) |
          (bt ? 1u << 16 : 0u);
+}
+
+// One thread of a converged warp, the same one every time.  The MMA warp runs its loop
+// converged and branches on this for each batch: 64 cycles an MMA here, which is what the
+// tensor core takes; with the issue predicated on lane 0 instead it was 73 alone and 85
+// beside busy warps.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]: A holds two 16-bit values a column.
@@ -525,23 +541,19 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     if (nq > 0 && !tc::mbar_wait(&bar->q_full, (nq - 1) & 1)) *gave_up = 1;
   } else if (warp == 8) {
     // ------------------------------------------------------------------ MMA
-    uint32_t n = 0, piece = 0;      // tiles used, pieces
-    uint32_t pc = 0;                // parity of each stream's P tiles
+    uint32_t base = 0, piece = 0;  // ring tiles of earlier pieces, pieces
+    uint32_t pc = 0;               // parity of each stream's P tiles
     constexpr uint32_t idS = tc::idesc16<T>(128, 128, false);
     constexpr uint32_t idO = tc::idesc16<T>(128, H, true);
     const uint64_t q_desc = tc::sdesc_k128(tc::smem_addr(sq));
     const uint64_t k_desc = tc::sdesc_k128(tc::smem_addr(ring));
     const uint64_t v_desc = tc::sdesc_mn128(tc::smem_addr(ring));
-    auto slot_wait = [&](uint32_t i) {
-      ok = ok && tc::mbar_wait_or(bar->full + i % Cfg::SLOTS, (i / Cfg::SLOTS) & 1, gave_up);
-      ok = __all_sync(0xffffffffu, ok);
-      tc::fence_after_sync();
+    // Only the elected thread's `ok` counts, so the lanes need no vote.
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      ok = ok && tc::mbar_wait_or(b, parity, gave_up);
     };
     // values nobody sees become 0, so that 0 * value is 0 whatever the slot held
-    auto clear_v = [&](uint32_t i, int tile) {
-      const int lo = min(max(w.k.lo - tile * PA_KT, 0), PA_KT);
-      const int hi = min(max(w.k.hi - tile * PA_KT, lo), PA_KT);
-      if (!ok || (lo == 0 && hi == PA_KT)) return;
+    auto clear_v = [&](uint32_t i, int lo, int hi) {
       uint8_t* v = ring + (i % Cfg::SLOTS) * Cfg::TILE;
       for (int ch = 0; ch < Cfg::CH; ++ch) {
         uint8_t* vc = v + ch * PA_CHUNK;
@@ -554,68 +566,79 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       __syncwarp();
     };
     for (; w.next(p); ++piece) {
-      const bool pair = w.pair(p);
-      const int t0 = w.k.t0 + w.first, steps = pair ? 2 * w.count : w.count;
-      ok = ok && tc::mbar_wait_or(&bar->q_full, piece & 1, gave_up);
-      ok = __all_sync(0xffffffffu, ok);
-      uint32_t v = 0, kk = 0;  // ring tiles in use
+      // through a reduction, whose result the compiler knows to be the same in every lane
+      const bool pair = __reduce_max_sync(0xffffffffu, (unsigned)w.pair(p)) != 0;
+      const int count = __reduce_max_sync(0xffffffffu, w.count);
+      const int key0 = __reduce_max_sync(0xffffffffu, (w.k.t0 + w.first) * PA_KT);
+      const int klo = __reduce_max_sync(0xffffffffu, w.k.lo) - key0;
+      const int khi = __reduce_max_sync(0xffffffffu, w.k.hi) - key0;
+      const int steps = pair ? 2 * count : count;
+      wait(&bar->q_full, piece & 1);
       // Step u adds P V of stream u & 1 and issues the same stream's next scores, two steps
       // ahead.  Solo: step u is key tile u.  Pair: steps 2 i and 2 i + 1 are key tile i.
+      // The ring holds K0 V0 K1 V1 .. for a pair and K0 K1 V0 K2 V1 K3 .. else.
+      uint32_t vs = 0, ks = 0;
 #pragma unroll 1
       for (int u = -2; u < steps; ++u) {
         const int t = u & 1;
+        const bool more = u + 2 < steps;
+        // the tiles first: their waits are over long before the softmax's
+        if (u >= 0 && (!pair || t == 0)) {
+          vs = base + (pair ? u + 1 : min(steps, 2) + u + min(u, max(steps - 2, 0)));
+          wait(bar->full + vs % Cfg::SLOTS, (vs / Cfg::SLOTS) & 1);
+          const int at = (pair ? u >> 1 : u) * PA_KT;
+          const int lo = min(max(klo - at, 0), PA_KT), hi = min(max(khi - at, lo), PA_KT);
+          if (lo > 0 || hi < PA_KT) clear_v(vs, lo, hi);
+        }
+        if (more && (!pair || t == 0)) {
+          ks = base + (pair ? u + 2 : u < 0 ? u + 2 : 2 * u + 3);
+          wait(bar->full + ks % Cfg::SLOTS, (ks / Cfg::SLOTS) & 1);
+        }
         if (u >= 0) {
-          if (!pair || t == 0) {
-            v = n++;
-            slot_wait(v);
-            clear_v(v, t0 + (pair ? u >> 1 : u));
-          }
+          const uint64_t vd = v_desc + (uint64_t)((vs % Cfg::SLOTS) * (Cfg::TILE >> 4));
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {  // O_t += P_t V, 64 keys at a time
-            ok = ok && tc::mbar_wait_or(bar->p_full + 2 * t + hf, (pc >> t) & 1, gave_up);
-            ok = __all_sync(0xffffffffu, ok);
+            wait(bar->p_full + 2 * t + hf, (pc >> t) & 1);
             tc::fence_after_sync();
-            if (ok && lane == 0) {
-              const uint64_t vd = v_desc + (uint64_t)((v % Cfg::SLOTS) * (Cfg::TILE >> 4));
+            if (tc::elect() && ok) {
 #pragma unroll
               for (int k = 4 * hf; k < 4 * hf + 4; ++k)
                 tc::mma_ts(tmem + 256 + t * H, tmem + t * 128 + k * 8, vd + k * (2048 >> 4), idO,
                            u >= 2 || k != 0);
             }
+            __syncwarp();
           }
           pc ^= 1u << t;
-          if (ok && lane == 0) {
-            if (u + 2 >= steps) tc::mma_commit(bar->o_full + t);
-            if (!pair || t == 1) tc::mma_commit(bar->empty + v % Cfg::SLOTS);
-          }
-          __syncwarp();
         }
-        if (u + 2 < steps) {
-          if (!pair || t == 0) {
-            kk = n++;
-            slot_wait(kk);
-          }
-          if (ok && lane == 0) {  // S_t = Q K^T
+        if (tc::elect() && ok) {
+          if (more) {
+            tc::fence_after_sync();
             const uint64_t qd = q_desc + (uint64_t)(pair && t ? Cfg::TILE >> 4 : 0);
-            const uint64_t kd = k_desc + (uint64_t)((kk % Cfg::SLOTS) * (Cfg::TILE >> 4));
+            const uint64_t kd = k_desc + (uint64_t)((ks % Cfg::SLOTS) * (Cfg::TILE >> 4));
 #pragma unroll
-            for (int k = 0; k < 4 * Cfg::CH; ++k) {
+            for (int k = 0; k < 4 * Cfg::CH; ++k) {  // S_t = Q K^T
               const uint32_t o = ((k >> 2) * PA_CHUNK + (k & 3) * 32) >> 4;
               tc::mma_bf16(tmem + t * 128, qd + o, kd + o, idS, k != 0);
             }
             tc::mma_commit(bar->s_full + t);
-            if (!pair || t == 1) tc::mma_commit(bar->empty + kk % Cfg::SLOTS);
+            if (!pair || t == 1) tc::mma_commit(bar->empty + ks % Cfg::SLOTS);
             if (u + 3 == steps) tc::mma_commit(&bar->q_empty);
           }
-          __syncwarp();
+          if (u >= 0) {
+            if (!more) tc::mma_commit(bar->o_full + t);
+            if (!pair || t == 1) tc::mma_commit(bar->empty + vs % Cfg::SLOTS);
+          }
         }
+        __syncwarp();
       }
+      base += 2 * count;
     }
     // nothing of the tensor cores' may be in flight when TMEM is freed
-    if (lane == 0) {
+    if (tc::elect()) {
       tc::mma_commit(&bar->done);
       if (!tc::mbar_wait(&bar->done, 0)) *gave_up = 1;
     }
+    __syncwarp();
   }
   } else {
     // ------------------------------------------------------------------ softmax
