@@ -578,24 +578,32 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       // ahead.  Solo: step u is key tile u.  Pair: steps 2 i and 2 i + 1 are key tile i.
       // The ring holds K0 V0 K1 V1 .. for a pair and K0 K1 V0 K2 V1 K3 .. else.
       uint32_t vs = 0, ks = 0;
+      uint64_t vd = 0, kd = 0;
+      // key tiles of the piece that hold keys nobody sees: the first, the last or none
+      const int cut_lo = klo > 0 ? 0 : -1, cut_hi = khi < count * PA_KT ? count - 1 : -1;
 #pragma unroll 1
       for (int u = -2; u < steps; ++u) {
         const int t = u & 1;
         const bool more = u + 2 < steps;
         // the tiles first: their waits are over long before the softmax's
-        if (u >= 0 && (!pair || t == 0)) {
-          vs = base + (pair ? u + 1 : min(steps, 2) + u + min(u, max(steps - 2, 0)));
-          wait(bar->full + vs % Cfg::SLOTS, (vs / Cfg::SLOTS) & 1);
-          const int at = (pair ? u >> 1 : u) * PA_KT;
-          const int lo = min(max(klo - at, 0), PA_KT), hi = min(max(khi - at, lo), PA_KT);
-          if (lo > 0 || hi < PA_KT) clear_v(vs, lo, hi);
-        }
-        if (more && (!pair || t == 0)) {
-          ks = base + (pair ? u + 2 : u < 0 ? u + 2 : 2 * u + 3);
-          wait(bar->full + ks % Cfg::SLOTS, (ks / Cfg::SLOTS) & 1);
+        if (!pair || t == 0) {
+          if (u >= 0) {
+            vs = base + (pair ? u + 1 : min(steps, 2) + u + min(u, max(steps - 2, 0)));
+            vd = v_desc + (uint64_t)((vs % Cfg::SLOTS) * (Cfg::TILE >> 4));
+            wait(bar->full + vs % Cfg::SLOTS, (vs / Cfg::SLOTS) & 1);
+            const int tile = pair ? u >> 1 : u;
+            if (tile == cut_lo || tile == cut_hi) {
+              const int lo = min(max(klo - tile * PA_KT, 0), PA_KT);
+              clear_v(vs, lo, min(max(khi - tile * PA_KT, lo), PA_KT));
+            }
+          }
+          if (more) {
+            ks = base + (pair ? u + 2 : u < 0 ? u + 2 : 2 * u + 3);
+            kd = k_desc + (uint64_t)((ks % Cfg::SLOTS) * (Cfg::TILE >> 4));
+            wait(bar->full + ks % Cfg::SLOTS, (ks / Cfg::SLOTS) & 1);
+          }
         }
         if (u >= 0) {
-          const uint64_t vd = v_desc + (uint64_t)((vs % Cfg::SLOTS) * (Cfg::TILE >> 4));
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {  // O_t += P_t V, 64 keys at a time
             wait(bar->p_full + 2 * t + hf, (pc >> t) & 1);
@@ -614,7 +622,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           if (more) {
             tc::fence_after_sync();
             const uint64_t qd = q_desc + (uint64_t)(pair && t ? Cfg::TILE >> 4 : 0);
-            const uint64_t kd = k_desc + (uint64_t)((ks % Cfg::SLOTS) * (Cfg::TILE >> 4));
 #pragma unroll
             for (int k = 0; k < 4 * Cfg::CH; ++k) {  // S_t = Q K^T
               const uint32_t o = ((k >> 2) * PA_CHUNK + (k & 3) * 32) >> 4;
@@ -676,11 +683,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           float s[128];
           const bool edge = key0 < lo_max || key0 + PA_KT > hi_min;
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          tc::tmem_ld32_async(ts, s);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {  // the next 32 scores arrive while these are compared
+          for (int q = 0; q < 4; ++q) tc::tmem_ld32_async(ts + 32 * q, s + 32 * q);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
             tc::tmem_wait32(s + 32 * q);
-            if (q < 3) tc::tmem_ld32_async(ts + 32 * (q + 1), s + 32 * (q + 1));
             if (edge) {
               const int a = lo - key0, z = hi - key0;
 #pragma unroll
