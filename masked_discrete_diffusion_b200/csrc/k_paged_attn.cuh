@@ -115,12 +115,54 @@ __device__ __forceinline__ PagedKeys paged_keys(const PagedAttnParams& p, const 
   return k;
 }
 
-__device__ __forceinline__ long long paged_work(const PagedAttnParams& p, const PagedSeq& s) {
+// Line length of the sequence of each lane (0 items: 0).  A lane adds up its own items when
+// they are few or alike; longer causal chunks are added up by the whole warp, one at a time.
+__device__ __forceinline__ long long paged_work(const PagedAttnParams& p, const PagedSeq& s,
+                                                int lane) {
+  const int step = 2 * p.T, items = (s.ql + step - 1) / step;
   long long w = 0;
-  for (int i0 = 0; i0 < s.ql; i0 += 2 * p.T)
-    w += paged_keys(p, s, i0, min(2 * p.T, s.ql - i0)).n + PA_ITEM;
+  const bool many = items > 4 && s.causal;
+  if (items > 0 && !s.causal) {
+    w = (long long)items * (paged_keys(p, s, 0, 1).n + PA_ITEM);  // all see the same keys
+  } else if (!many) {
+#pragma unroll 1
+    for (int i = 0; i < items; ++i)
+      w += paged_keys(p, s, i * step, min(step, s.ql - i * step)).n + PA_ITEM;
+  }
+#pragma unroll 1
+  for (unsigned m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
+    const int src = __ffs(m) - 1;
+    PagedSeq x;
+    x.ql = __shfl_sync(0xffffffffu, s.ql, src);
+    x.past = __shfl_sync(0xffffffffu, s.past, src);
+    x.kv = __shfl_sync(0xffffffffu, s.kv, src);
+    x.causal = 1;
+    const int n = (x.ql + step - 1) / step;
+    long long v = 0;
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32)
+      v += paged_keys(p, x, i * step, min(step, x.ql - i * step)).n + PA_ITEM;
+    v = warp_sum(v);
+    if (lane == src) w = v;
+  }
   return w * p.hkv;
 }
+
+// An even split of `total` into `parts`: the first `rem` have q + 1.
+struct PagedSplit {
+  unsigned long long q, rem;
+  __device__ __forceinline__ PagedSplit(unsigned long long total, unsigned parts) {
+    q = total / parts;
+    rem = total - q * parts;
+  }
+  __device__ __forceinline__ long long start(unsigned c) const {
+    return (long long)(c * q + min((unsigned long long)c, rem));
+  }
+  __device__ __forceinline__ int owner(unsigned long long at) const {  // the part that holds it
+    const unsigned long long cut = rem * (q + 1);
+    return (int)(at < cut ? at / (q + 1) : rem + (at - cut) / q);
+  }
+};
 
 // Walks the pieces of a CTA's part of the line.
 struct PagedWalk {
@@ -137,29 +179,49 @@ struct PagedWalk {
     nt = min(2 * p.T, s.ql - i0);
     k = paged_keys(p, s, i0, nt);
   }
+  // `count` units from unit `skip` of sequence b on (a whole warp: 32 items at a time).
   __device__ __forceinline__ void start(const PagedAttnParams& p, int b, long long skip,
-                                        long long count_) {
+                                        long long count_, int lane) {
     left = count_;
     if (left <= 0) return;
     paged_seq(p, b, &s);
-    i0 = 0;
-    item(p);
-    while (skip >= (long long)(k.n + PA_ITEM) * p.hkv && i0 + 2 * p.T < s.ql) {
-      skip -= (long long)(k.n + PA_ITEM) * p.hkv;
-      i0 += 2 * p.T;
-      item(p);
+    const int step = 2 * p.T, items = (s.ql + step - 1) / step;
+    int at = 0;
+#pragma unroll 1
+    for (int i = 0; i < items; i += 32) {
+      const int mine = i + lane;
+      long long len = 0;
+      if (mine < items)
+        len = (long long)(paged_keys(p, s, mine * step, min(step, s.ql - mine * step)).n +
+                          PA_ITEM) * p.hkv;
+      long long incl = len;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned before = __ballot_sync(0xffffffffu, mine < items && incl <= skip);
+      const int n = __popc(before);
+      at = min(i + n, items - 1);
+      if (n > 0) skip -= __shfl_sync(0xffffffffu, incl, n - 1);
+      if (n < 32) break;
     }
-    g = (int)(skip / (k.n + PA_ITEM));
-    off = (int)(skip % (k.n + PA_ITEM));
+    i0 = at * step;
+    item(p);
+    const unsigned long long len = k.n + PA_ITEM;
+    g = (int)min((unsigned long long)skip / len, (unsigned long long)p.hkv - 1);
+    off = (int)min((unsigned long long)skip - g * len, len - 1);
   }
   // Prepares the next piece; false at the end of the part.
   __device__ __forceinline__ bool next(const PagedAttnParams& p) {
+#pragma unroll 1
     while (left > 0) {
       if (off == k.n + PA_ITEM) {  // the item is done: next head, tokens, sequence
         off = 0;
         if (++g == p.hkv) {
           g = 0;
           i0 += 2 * p.T;
+#pragma unroll 1
           while (i0 >= s.ql) {
             if (s.b + 1 >= p.B) {  // only if the lengths change under the call
               left = 0;
@@ -312,6 +374,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
+// x << n, 0 for n of 32 or more.
+__device__ __forceinline__ unsigned shl(unsigned x, unsigned n) {
+  unsigned y;
+  asm("shl.b32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(n));
+  return y;
+}
+
 // Two fp32 values in a register pair, for the packed instructions.
 __device__ __forceinline__ uint64_t f2(float a, float b) {
   uint64_t r;
@@ -347,7 +416,7 @@ struct PagedPlan {
   int b;
   int32_t gave_up;
   long long sums[PA_THREADS / 32];
-  int32_t bad[4];  // a page out of range, by piece modulo 4
+  int32_t bad[8];  // a page out of range, by piece modulo 8
 };
 
 struct PagedBars {
@@ -367,25 +436,25 @@ __device__ __forceinline__ int paged_parts(long long total) {
 __device__ __forceinline__ int paged_plan(const PagedAttnParams& p, PagedPlan* plan, int c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long base = 0, mine = 0, incl = 0;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     long long start = 0;
     if (pass == 1) {
       const int parts = paged_parts(base);
       if (base == 0 || c >= parts) return parts;
-      start = base * c / parts;
+      start = PagedSplit(base, parts).start(c);
       if (tid == 0) plan->total = base;
       base = 0;
     }
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += PA_THREADS) {
       const int b = b0 + tid;
       if (pass == 0 || p.B > PA_THREADS) {  // up to one sequence a thread: once is enough
         mine = 0;
-        if (b < p.B) {
-          PagedSeq s;
-          if (paged_seq(p, b, &s) && pass == 0 && c == 0 && p.err)
-            atomicOr(p.err, DG_PAGED_BAD_BATCH);
-          mine = paged_work(p, s);
-        }
+        PagedSeq s = {};
+        if (b < p.B && paged_seq(p, b, &s) && pass == 0 && c == 0 && p.err)
+          atomicOr(p.err, DG_PAGED_BAD_BATCH);
+        mine = paged_work(p, s, lane);
         incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -395,9 +464,11 @@ __device__ __forceinline__ int paged_plan(const PagedAttnParams& p, PagedPlan* p
         __syncthreads();
         if (lane == 31) plan->sums[warp] = incl;
         __syncthreads();
+#pragma unroll 1
         for (int w = 0; w < warp; ++w) incl += plan->sums[w];
       }
       long long all = 0;
+#pragma unroll 1
       for (int w = 0; w < PA_THREADS / 32; ++w) all += plan->sums[w];
       if (pass == 1 && start >= base + incl - mine && start < base + incl) {
         plan->b = b;
@@ -454,7 +525,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     }
     tc::fence_mbar_init();
     plan->gave_up = 0;
-    for (int i = 0; i < 4; ++i) plan->bad[i] = 0;
+    for (int i = 0; i < 8; ++i) plan->bad[i] = 0;
   }
   if (warp == 8) tc::tmem_alloc(&tslot, 512);
   if (tid == PA_THREADS - 32) {
@@ -474,9 +545,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   if (tid == 0) p.rec[c].valid = 0;
   const bool idle = c >= parts;
   const long long total = idle ? 0 : plan->total;
+  const PagedSplit split(total, max(parts, 1));
   PagedWalk w;
   w.start(p, idle ? 0 : plan->b, idle ? 0 : plan->skip,
-          idle ? 0 : total * (c + 1) / parts - total * c / parts);
+          idle ? 0 : split.start(c + 1) - split.start(c), lane);
   bool ok = true;
 
   if (warp >= 8) {
@@ -485,52 +557,73 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     // ------------------------------------------------------------------ TMA
     uint32_t n = 0, nq = 0, piece = 0;  // tiles and row tiles requested, pieces
     const int rows = min(1 << p.page_log2, PA_KT), npg = PA_KT / rows;
+    const int pg = lane & (npg - 1), ch = lane / npg;  // this lane's page of a tile, and chunk
+    // Page numbers: a lane holds one of 32 consecutive ones, of two such blocks, so the table
+    // is read a block ahead of its use.  (K runs at most two tiles, 16 pages, ahead of V.)
+    int e0 = -1, e1 = -1, blk = 0;
+    auto entries = [&](int k) {
+      const long long key = ((long long)k * 32 + lane) << p.page_log2;
+      return key < w.k.hi && key + (1LL << p.page_log2) > w.k.lo
+                 ? p.table[(long long)w.s.b * p.max_pages + k * 32 + lane]
+                 : -1;
+    };
     auto load = [&](const CUtensorMap* map, int tile) {
+      const int key = tile * PA_KT + pg * rows, page = key >> p.page_log2;
+      const int first = (tile * PA_KT) >> (p.page_log2 + 5);  // a tile's pages share a block
+      if (first > blk + 1) {
+        e0 = e1;
+        e1 = entries(++blk + 1);
+      }
+      const int in0 = __shfl_sync(0xffffffffu, e0, page & 31);
+      const int in1 = __shfl_sync(0xffffffffu, e1, page & 31);
+      const int id = first == blk ? in0 : in1;
+      const bool need = ch < Cfg::CH && key < w.k.hi && key + rows > w.k.lo;
+      const bool good = need && id >= 0 && id < p.n_pages;
+      const unsigned mask = __ballot_sync(0xffffffffu, good);
+      const bool bad = __any_sync(0xffffffffu, need && !good);
       const int s = n % Cfg::SLOTS;
       ok = ok && tc::mbar_wait_or(bar->empty + s, ((n / Cfg::SLOTS) & 1) ^ 1, gave_up);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
-      const int pg = lane & (npg - 1);
-      const int key = tile * PA_KT + pg * rows;
-      const bool need = lane < npg * Cfg::CH && key < w.k.hi && key + rows > w.k.lo;
-      const int id = need ? p.table[(long long)w.s.b * p.max_pages + (key >> p.page_log2)] : -1;
-      const bool good = need && id >= 0 && id < p.n_pages;
-      const unsigned mask = __ballot_sync(0xffffffffu, good);
-      if (__any_sync(0xffffffffu, need && !good) && lane == 0) {
-        plan->bad[piece & 3] = 1;
-        if (p.err) atomicOr(p.err, DG_PAGED_BAD_PAGE);
+      if (lane == 0) {
+        if (bad) {
+          plan->bad[piece & 7] = 1;
+          if (p.err) atomicOr(p.err, DG_PAGED_BAD_PAGE);
+        }
+        tc::mbar_expect_tx(bar->full + s, __popc(mask) * rows * 128);
       }
-      if (lane == 0) tc::mbar_expect_tx(bar->full + s, __popc(mask) * rows * 128);
       __syncwarp();
-      if (good) {
-        const int ch = lane / npg;
+      if (good)
         tc::tma_load_4d(ring + s * Cfg::TILE + ch * PA_CHUNK + pg * rows * 128, map, bar->full + s,
                         ch * 64, key & ((1 << p.page_log2) - 1), w.g, id);
-      }
       ++n;
     };
     for (; w.next(p); ++piece) {
       const bool pair = w.pair(p);
-      ok = ok && tc::mbar_wait_or(&bar->q_empty, (piece & 1) ^ 1, gave_up);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        const int tiles = pair ? 2 : 1;
-        ++nq;
-        if (lane == 0) {
-          plan->bad[piece & 3] = 0;
-          tc::mbar_expect_tx(&bar->q_full, tiles * Cfg::CH * p.G * p.T * 128);
-        }
-        __syncwarp();
-        if (lane < tiles * Cfg::CH) {
-          const int t = lane / Cfg::CH, ch = lane % Cfg::CH;
-          tc::tma_load_3d(sq + t * Cfg::TILE + ch * PA_CHUNK, &mq, &bar->q_full, ch * 64,
-                          w.g * p.G, w.s.q0 + w.i0 + t * p.T);
-        }
-      }
-      // in the order of first use (the MMA warp's loop)
       const int t0 = w.k.t0 + w.first, steps = pair ? 2 * w.count : w.count;
+      blk = (t0 * PA_KT) >> (p.page_log2 + 5);
+      e0 = entries(blk);
+      e1 = entries(blk + 1);
+      if (lane == 0) plan->bad[piece & 7] = 0;
+      // in the order of first use (the MMA warp's loop); the first keys go before the rows,
+      // whose buffer the last piece may still hold
 #pragma unroll 1
       for (int u = -2; u < steps; ++u) {
+        if (u == 0) {
+          ok = ok && tc::mbar_wait_or(&bar->q_empty, (piece & 1) ^ 1, gave_up);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            const int tiles = pair ? 2 : 1;
+            ++nq;
+            if (lane == 0) tc::mbar_expect_tx(&bar->q_full, tiles * Cfg::CH * p.G * p.T * 128);
+            __syncwarp();
+            if (lane < tiles * Cfg::CH) {
+              const int t = lane / Cfg::CH, qc = lane % Cfg::CH;
+              tc::tma_load_3d(sq + t * Cfg::TILE + qc * PA_CHUNK, &mq, &bar->q_full, qc * 64,
+                              w.g * p.G, w.s.q0 + w.i0 + t * p.T);
+            }
+          }
+        }
         if (pair && (u & 1)) continue;
         if (u >= 0) load(&mv, t0 + (pair ? u >> 1 : u));
         if (u + 2 < steps) load(&mk, t0 + (pair ? (u + 2) >> 1 : u + 2));
@@ -555,10 +648,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     // values nobody sees become 0, so that 0 * value is 0 whatever the slot held
     auto clear_v = [&](uint32_t i, int lo, int hi) {
       uint8_t* v = ring + (i % Cfg::SLOTS) * Cfg::TILE;
+#pragma unroll 1
       for (int ch = 0; ch < Cfg::CH; ++ch) {
         uint8_t* vc = v + ch * PA_CHUNK;
+#pragma unroll 1
         for (int x = lane; x < lo * 8; x += 32)
           *reinterpret_cast<uint4*>(vc + x * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
         for (int x = hi * 8 + lane; x < PA_KT * 8; x += 32)
           *reinterpret_cast<uint4*>(vc + x * 16) = make_uint4(0, 0, 0, 0);
       }
@@ -689,9 +785,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           for (int q = 0; q < 4; ++q) {
             tc::tmem_wait32(s + 32 * q);
             if (edge) {
-              const int a = lo - key0, z = hi - key0;
+              // bits lo .. hi - 1 of this chunk (a shift by 32 or more gives 0)
+              const unsigned a = max(lo - key0 - 32 * q, 0), z = max(hi - key0 - 32 * q, 0);
+              const unsigned seen = shl(0xffffffffu, a) & ~shl(0xffffffffu, z);
 #pragma unroll
-              for (int x = 32 * q; x < 32 * q + 32; ++x) s[x] = x >= a && x < z ? s[x] : -INFINITY;
+              for (int x = 0; x < 32; ++x)
+                s[32 * q + x] = seen >> x & 1 ? s[32 * q + x] : -INFINITY;
             }
 #pragma unroll
             for (int x = 0; x < 32; x += 8)
@@ -760,11 +859,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
       }
       // ---- the piece's rows: whole items to out, cut ones to the workspace
-      const bool bad = plan->bad[piece & 3] != 0;
+      const bool bad = plan->bad[piece & 7] != 0;
       const bool begins = w.first == 0, ends = w.first + w.count == w.k.n;
-      // this row in out (-1: none), and in the workspace
-      const long long row_at =
-          live ? ((long long)w.s.q0 + w.i0 + i0 + tok) * p.hq + w.g * p.G + head : -1;
+      // this row within the item's rows of out (-1: none), and in the workspace
+      const int row_at = live ? (i0 + tok) * p.hq + w.g * p.G + head : -1;
       const long long piece_at = (long long)c * 2 + (begins ? 1 : 0);
       const int piece_row = (pair ? t * 128 : 0) + r;
       float w0 = 1.f, w1 = 0.f;  // weights of this stream's and the other's O
@@ -783,26 +881,26 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       const bool whole = begins && ends;
       if (work && ok) {
         tc::fence_after_sync();
-        const int c_lo = pair ? 0 : t * (H / 2), c_hi = pair ? H : c_lo + H / 2;
         const bool two = !pair && w.count > 1;
+        const uint32_t o_a = pair ? to : tmem + 256 + lanes, o_b = tmem + 256 + H + lanes;
+        const float f0 = whole ? w0 * inv : w0, f1 = whole ? w1 * inv : w1;
+        T* out = static_cast<T*>(p.out) + ((long long)w.s.q0 + w.i0) * p.hq * H;
+        // one short loop: the code of a piece's end runs once a piece, and what of it the
+        // instruction cache has lost costs more than its latencies
+        const int q_end = pair ? H : (t + 1) * (H / 2);
 #pragma unroll 1
-        for (int q = c_lo; q < c_hi; q += 32) {
+        for (int q = pair ? 0 : t * (H / 2); q < q_end; q += 32) {
           float o[32];
-          if (pair) {
-            tc::tmem_ld32_async(to + q, o);
-            tc::tmem_wait32(o);
-          } else {
-            tc::tmem_ld32_async(tmem + 256 + lanes + q, o);
-            tc::tmem_wait32(o);
+          tc::tmem_ld32_async(o_a + q, o);
+          tc::tmem_wait32(o);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = w0 == 0.f ? 0.f : o[x] * w0;
-            if (two) {
-              float o2[32];
-              tc::tmem_ld32_async(tmem + 256 + H + lanes + q, o2);
-              tc::tmem_wait32(o2);
+          for (int x = 0; x < 32; ++x) o[x] *= f0;
+          if (two) {
+            float o2[32];
+            tc::tmem_ld32_async(o_b + q, o2);
+            tc::tmem_wait32(o2);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] += w1 == 0.f ? 0.f : o2[x] * w1;
-            }
+            for (int x = 0; x < 32; ++x) o[x] = fmaf(o2[x], f1, o[x]);
           }
           if (whole) {
             // through this warp's 2 KB of shared memory, so that a store instruction
@@ -810,18 +908,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               stage[lane * 4 + (x ^ ((lane >> 1) & 3))] =
-                  make_uint4(pack2<T>(o[8 * x] * inv, o[8 * x + 1] * inv),
-                             pack2<T>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
-                             pack2<T>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
-                             pack2<T>(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
+                  make_uint4(pack2<T>(o[8 * x], o[8 * x + 1]), pack2<T>(o[8 * x + 2], o[8 * x + 3]),
+                             pack2<T>(o[8 * x + 4], o[8 * x + 5]),
+                             pack2<T>(o[8 * x + 6], o[8 * x + 7]));
             __syncwarp();
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int rr = 8 * x + (lane >> 2);
-              const uint4 v = stage[rr * 4 + ((lane & 3) ^ ((rr >> 1) & 3))];
-              const long long at = __shfl_sync(0xffffffffu, row_at, rr);
-              if (at >= 0)
-                reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * H + q)[lane & 3] = v;
+              const uint4 y = stage[rr * 4 + ((lane & 3) ^ ((rr >> 1) & 3))];
+              const int at = __shfl_sync(0xffffffffu, row_at, rr);
+              if (at >= 0) reinterpret_cast<uint4*>(out + (long long)at * H + q)[lane & 3] = y;
             }
             __syncwarp();
           } else if (live) {
@@ -837,7 +933,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         if (!whole)
           p.part_ml[piece_at * p.part_rows + piece_row] = make_float2(M, L);
         else if (p.lse)
-          p.lse[row_at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          p.lse[((long long)w.s.q0 + w.i0) * p.hq + row_at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
       }
       if (!pair) {
         // both warpgroups have read both accumulators and xml
@@ -846,10 +942,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       if (tid == 0 && begins && !ends) {
         // the line's position of the item's end gives the last CTA that holds a piece
-        const long long at = total * (c + 1) / parts - w.left - w.off + w.k.n + PA_ITEM;
+        const long long end = split.start(c + 1) - w.left - w.off + w.k.n + PA_ITEM;
         PagedRec rec;
         rec.valid = 1;
-        rec.last = (int)((at * parts - 1) / total);
+        rec.last = split.owner(end - 1);
         rec.row0 = w.s.q0 + w.i0;
         rec.ntok = w.nt;
         rec.g = w.g;
