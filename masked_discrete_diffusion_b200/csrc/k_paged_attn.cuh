@@ -14,7 +14,8 @@
 //
 // Split.  All items form one line, each as long as its key tiles plus PA_ITEM (what filling
 // and emptying the pipeline for it costs, in tiles); 148 CTAs take equal contiguous parts of
-// it, so no length mix leaves SMs idle.  A CTA's part is a run of whole items with a cut one at
+// it, so no length mix leaves SMs idle.  (Items that are all alike stay whole where that costs
+// less than cutting them: eight canvases' 128 items of 10 tiles, 47 -> UNIF us.)  A CTA's part is a run of whole items with a cut one at
 // either end; cut pieces leave (m, l, O) in the workspace and paged_merge_kernel adds an
 // item's pieces in the order of the line (the same bits every time).  Each CTA finds its
 // part from the lengths on the device: no host plan, and a captured graph follows them.
@@ -38,6 +39,9 @@ constexpr int PA_CTAS = 148;
 constexpr int PA_THREADS = 384;  // 12 warps: 8 softmax, MMA, TMA, 2 that only help to plan
 constexpr int PA_KT = 128;                 // keys a tile
 constexpr int PA_ITEM = 2;                 // an item's fixed cost in tiles
+constexpr int PA_CUT = 2;                  // no cut leaves fewer tiles on a side
+constexpr int PA_PART = 5;                 // shortest part of the line
+constexpr int PA_MERGE = 5;                // what cutting items costs a call, in tiles
 constexpr uint32_t PA_CHUNK = 128 * 128;   // 128 rows of 64 channels
 
 template <int H> struct PagedCfg {
@@ -115,20 +119,23 @@ __device__ __forceinline__ PagedKeys paged_keys(const PagedAttnParams& p, const 
   return k;
 }
 
-// Line length of the sequence of each lane (0 items: 0).  A lane adds up its own items when
-// they are few or alike; longer causal chunks are added up by the whole warp, one at a time.
+// Line length of the sequence of each lane (0 items: 0), and the extremes of its items'
+// tiles.  A lane adds up its own items when they are few or alike; longer causal chunks are
+// added up by the whole warp, one at a time.
 __device__ __forceinline__ long long paged_work(const PagedAttnParams& p, const PagedSeq& s,
-                                                int lane) {
+                                                int lane, int* n_min, int* n_max) {
   const int step = 2 * p.T, items = (s.ql + step - 1) / step;
   long long w = 0;
   const bool many = items > 4 && s.causal;
-  if (items > 0 && !s.causal) {
-    w = (long long)items * (paged_keys(p, s, 0, 1).n + PA_ITEM);  // all see the same keys
-  } else if (!many) {
+  const int alone = many ? 0 : s.causal ? items : min(items, 1);
 #pragma unroll 1
-    for (int i = 0; i < items; ++i)
-      w += paged_keys(p, s, i * step, min(step, s.ql - i * step)).n + PA_ITEM;
+  for (int i = 0; i < alone; ++i) {
+    const int n = paged_keys(p, s, i * step, min(step, s.ql - i * step)).n;
+    *n_min = min(*n_min, n);
+    *n_max = max(*n_max, n);
+    w += n + PA_ITEM;
   }
+  if (!s.causal) w *= items;  // all its items see the same keys
 #pragma unroll 1
   for (unsigned m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
     const int src = __ffs(m) - 1;
@@ -137,32 +144,61 @@ __device__ __forceinline__ long long paged_work(const PagedAttnParams& p, const 
     x.past = __shfl_sync(0xffffffffu, s.past, src);
     x.kv = __shfl_sync(0xffffffffu, s.kv, src);
     x.causal = 1;
-    const int n = (x.ql + step - 1) / step;
+    const int items_x = (x.ql + step - 1) / step;
     long long v = 0;
 #pragma unroll 1
-    for (int i = lane; i < n; i += 32)
-      v += paged_keys(p, x, i * step, min(step, x.ql - i * step)).n + PA_ITEM;
+    for (int i = lane; i < items_x; i += 32) {
+      const int n = paged_keys(p, x, i * step, min(step, x.ql - i * step)).n;
+      *n_min = min(*n_min, n);
+      *n_max = max(*n_max, n);
+      v += n + PA_ITEM;
+    }
     v = warp_sum(v);
     if (lane == src) w = v;
   }
   return w * p.hkv;
 }
 
-// An even split of `total` into `parts`: the first `rem` have q + 1.
+// The line's division: `parts` parts in whole multiples of `unit` tiles, the first `rem` of
+// them one multiple longer.
 struct PagedSplit {
   unsigned long long q, rem;
-  __device__ __forceinline__ PagedSplit(unsigned long long total, unsigned parts) {
-    q = total / parts;
-    rem = total - q * parts;
+  unsigned unit;
+  int parts;
+  // total 0: no parts.  n_min, n_max: the extremes of the items' tiles.
+  __device__ __forceinline__ PagedSplit(unsigned long long total, int n_min, int n_max) {
+    unsigned long long count = total;
+    unit = 1;
+    const unsigned long long least = (total + PA_PART - 1) / PA_PART;
+    parts = (int)min((unsigned long long)PA_CTAS, least);
+    if (n_min == n_max && total > 0) {
+      const unsigned len = n_min + PA_ITEM;
+      const unsigned long long items = total / len;
+      const unsigned long long whole = (items + PA_CTAS - 1) / PA_CTAS * len;
+      if (whole <= total / parts + PA_MERGE) {
+        unit = len;
+        count = items;
+        parts = (int)min((unsigned long long)PA_CTAS, items);
+      }
+    }
+    q = count / max(parts, 1);
+    rem = count - q * parts;
   }
   __device__ __forceinline__ long long start(unsigned c) const {
-    return (long long)(c * q + min((unsigned long long)c, rem));
+    return (long long)((c * q + min((unsigned long long)c, rem)) * unit);
   }
   __device__ __forceinline__ int owner(unsigned long long at) const {  // the part that holds it
+    at /= unit;
     const unsigned long long cut = rem * (q + 1);
     return (int)(at < cut ? at / (q + 1) : rem + (at - cut) / q);
   }
 };
+
+// Tiles of an item of n that lie before line unit u of it.
+__device__ __forceinline__ int paged_cut(int u, int n) {
+  const int x = u - PA_ITEM;
+  return x >= n ? n : x < PA_CUT ? 0 : x > n - PA_CUT ? n : x;
+}
 
 // Walks the pieces of a CTA's part of the line.
 struct PagedWalk {
@@ -234,11 +270,11 @@ struct PagedWalk {
         }
       }
       const int take = (int)min((long long)(k.n + PA_ITEM - off), left);
-      first = max(off - PA_ITEM, 0);
+      first = paged_cut(off, k.n);
       off += take;
       left -= take;
-      count = max(off - PA_ITEM, 0) - first;
-      if (count > 0) return true;  // else the part ends within the item's fixed cost
+      count = paged_cut(off, k.n) - first;
+      if (count > 0) return true;  // else the part has none of the item's tiles
     }
     return false;
   }
@@ -413,7 +449,7 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
 
 struct PagedPlan {
   long long total, skip;  // tiles of the line; tiles of sequence b before this CTA's part
-  int b;
+  int b, n_min, n_max;
   int32_t gave_up;
   long long sums[PA_THREADS / 32];
   int32_t bad[8];  // a page out of range, by piece modulo 8
@@ -426,35 +462,31 @@ struct PagedBars {
 };
 static_assert(sizeof(PagedPlan) + sizeof(PagedBars) <= 512, "fits the tail of shared memory");
 
-// CTAs that share a line of this length: as many as leave each a tile beyond the fixed cost.
-__device__ __forceinline__ int paged_parts(long long total) {
-  return (int)min((long long)PA_CTAS, (total + PA_ITEM) / (PA_ITEM + 1));
-}
-
-// Fills plan.total, and plan.b / plan.skip for the CTA that takes part `c` of `parts` (parts
-// follows from the total).  Every thread of the CTA calls it.
-__device__ __forceinline__ int paged_plan(const PagedAttnParams& p, PagedPlan* plan, int c) {
+// Fills plan.total, the extremes of the items' tiles, and plan.b / plan.skip, where the part of
+// CTA c begins (if it has one).  Every thread of the CTA calls it; a barrier must follow.
+__device__ __forceinline__ void paged_plan(const PagedAttnParams& p, PagedPlan* plan, int c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long base = 0, mine = 0, incl = 0;
+  long long base = 0, mine = 0, incl = 0, start = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    long long start = 0;
     if (pass == 1) {
-      const int parts = paged_parts(base);
-      if (base == 0 || c >= parts) return parts;
-      start = PagedSplit(base, parts).start(c);
       if (tid == 0) plan->total = base;
+      const PagedSplit split(base, plan->n_min, plan->n_max);
+      if (c >= split.parts) return;
+      start = split.start(c);
       base = 0;
     }
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += PA_THREADS) {
       const int b = b0 + tid;
       if (pass == 0 || p.B > PA_THREADS) {  // up to one sequence a thread: once is enough
-        mine = 0;
         PagedSeq s = {};
         if (b < p.B && paged_seq(p, b, &s) && pass == 0 && c == 0 && p.err)
           atomicOr(p.err, DG_PAGED_BAD_BATCH);
-        mine = paged_work(p, s, lane);
+        int n_min = 0x7fffffff, n_max = 0;
+        mine = paged_work(p, s, lane, &n_min, &n_max);
+        n_min = __reduce_min_sync(0xffffffffu, n_min);
+        n_max = __reduce_max_sync(0xffffffffu, n_max);
         incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -462,7 +494,13 @@ __device__ __forceinline__ int paged_plan(const PagedAttnParams& p, PagedPlan* p
           if (lane >= o) incl += v;
         }
         __syncthreads();
-        if (lane == 31) plan->sums[warp] = incl;
+        if (lane == 31) {
+          plan->sums[warp] = incl;
+          if (n_max > 0) {
+            atomicMin(&plan->n_min, n_min);
+            atomicMax(&plan->n_max, n_max);
+          }
+        }
         __syncthreads();
 #pragma unroll 1
         for (int w = 0; w < warp; ++w) incl += plan->sums[w];
@@ -477,7 +515,6 @@ __device__ __forceinline__ int paged_plan(const PagedAttnParams& p, PagedPlan* p
       base += all;
     }
   }
-  return paged_parts(base);
 }
 
 template <int N> __device__ __forceinline__ void reg_inc() {
@@ -525,6 +562,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     }
     tc::fence_mbar_init();
     plan->gave_up = 0;
+    plan->total = 0;
+    plan->n_min = 0x7fffffff;
+    plan->n_max = 0;
     for (int i = 0; i < 8; ++i) plan->bad[i] = 0;
   }
   if (warp == 8) tc::tmem_alloc(&tslot, 512);
@@ -535,7 +575,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   }
   pdl_enter();
   const int c = blockIdx.x;
-  const int parts = paged_plan(p, plan, c);
+  __syncthreads();  // the plan's initial values
+  paged_plan(p, plan, c);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -543,9 +584,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   volatile int32_t* gave_up = &plan->gave_up;
 
   if (tid == 0) p.rec[c].valid = 0;
-  const bool idle = c >= parts;
-  const long long total = idle ? 0 : plan->total;
-  const PagedSplit split(total, max(parts, 1));
+  const PagedSplit split(plan->total, plan->n_min, plan->n_max);
+  const bool idle = c >= split.parts;
   PagedWalk w;
   w.start(p, idle ? 0 : plan->b, idle ? 0 : plan->skip,
           idle ? 0 : split.start(c + 1) - split.start(c), lane);
@@ -942,10 +982,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       if (tid == 0 && begins && !ends) {
         // the line's position of the item's end gives the last CTA that holds a piece
-        const long long end = split.start(c + 1) - w.left - w.off + w.k.n + PA_ITEM;
+        const long long begin = split.start(c + 1) - w.left - w.off;
+        const int len = w.k.n + PA_ITEM;
+        int last = split.owner(begin + len - 1);
+        while (last > c && paged_cut((int)(split.start(last) - begin), w.k.n) == w.k.n) --last;
         PagedRec rec;
         rec.valid = 1;
-        rec.last = split.owner(end - 1);
+        rec.last = last;
         rec.row0 = w.s.q0 + w.i0;
         rec.ntok = w.nt;
         rec.g = w.g;
@@ -959,67 +1002,84 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
-// Adds the pieces of cut items: block (c, y) takes rows y * PM_ROWS .. of the item that
-// starts and does not end in CTA c.  Thread (row, 4 channels), rows fastest: a piece's
-// channels of 8 rows are one 128-byte line.
-constexpr int PM_ROWS = 8;
-
-template <class T, int H>
-__global__ void __launch_bounds__(PM_ROWS * H / 4) paged_merge_kernel(const PagedAttnParams p) {
-  __shared__ float wts[PM_ROWS][PA_CTAS];
+// Adds the pieces of cut items: block (c, y) takes rows 8 R y .. of the item that starts and
+// does not end in CTA c.  Thread (row, 4 channels) with 8 rows fastest, so that a piece's
+// channels of 8 rows are one 128-byte line, and R such rows a thread.  R = 4 for items of
+// two row tiles: mostly two pieces, 1,184 blocks in one wave (with R = 1 four waves, 17 us
+// against 12 from a cold L2); R = 1 for one: many pieces and few blocks (drafted tokens,
+// 16 against 12 us).
+template <class T, int H, int R>
+__global__ void __launch_bounds__(2 * H) paged_merge_kernel(const PagedAttnParams p) {
+  constexpr int PM_ROWS = 8 * R;
+  __shared__ float wts[PM_ROWS][PA_CTAS + 1];
   __shared__ float sums[PM_ROWS];
   pdl_enter();
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int WARPS = PM_ROWS * H / 128;
+  const int c = blockIdx.x, tid = threadIdx.x;
   const PagedRec rec = p.rec[c];
   if (!rec.valid) return;
   const int n = min(rec.last, PA_CTAS - 1) - c + 1;
   const int row0 = blockIdx.y * PM_ROWS;
-  // k-th piece: slot 1 of CTA c, then slot 0 of c + k
-  for (int i = warp; i < PM_ROWS; i += WARPS) {
-    const int row = row0 + i;
-    if (row >= p.part_rows) break;
+  auto row_at = [&](int row) -> long long {  // the row's place in out, -1: none
+    const int r = row & 127, tk = r / p.G, tok = (row >> 7) * p.T + tk;
+    if (row >= p.part_rows || tk >= p.T || tok >= rec.ntok) return -1;
+    return (long long)(rec.row0 + tok) * p.hq + rec.g * p.G + r % p.G;
+  };
+  // k-th piece: slot 1 of CTA c, then slot 0 of c + k.  Eight lanes a row.
+  for (int i = tid >> 3; i < PM_ROWS; i += H / 4) {
+    const int row = row0 + i, l8 = tid & 7;
+    const unsigned lanes = 0xffu << (tid & 24);
+    const bool in = row < p.part_rows;
     float M = -INFINITY;
-    for (int k = lane; k < n; k += 32)
+    for (int k = l8; in && k < n; k += 8)
       M = fmaxf(M, p.part_ml[((long long)(c + k) * 2 + (k == 0)) * p.part_rows + row].x);
-    M = warp_max(M);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, o));
     float L = 0.f;
-    for (int k = lane; k < n; k += 32) {
+    for (int k = l8; in && k < n; k += 8) {
       const float2 ml = p.part_ml[((long long)(c + k) * 2 + (k == 0)) * p.part_rows + row];
       const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
       wts[i][k] = wt;
       L += ml.y != ml.y ? ml.y : wt * ml.y;  // NaN: a page out of range
     }
-    L = warp_sum(L);
-    if (lane == 0) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(lanes, L, o);
+    if (l8 == 0) {
       sums[i] = L == 0.f ? 0.f : 1.f / L;
-      const int r = row & 127, tk = r / p.G, tok = (row >> 7) * p.T + tk;
-      if (p.lse && tk < p.T && tok < rec.ntok)
-        p.lse[(long long)(rec.row0 + tok) * p.hq + rec.g * p.G + r % p.G] =
-            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      const long long at = p.lse ? row_at(row) : -1;
+      if (at >= 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
   }
   __syncthreads();
-  const int i = threadIdx.x % PM_ROWS, q = threadIdx.x / PM_ROWS, row = row0 + i;
-  const int r = row & 127, tk = r / p.G, tok = (row >> 7) * p.T + tk;
-  if (row >= p.part_rows || tk >= p.T || tok >= rec.ntok) return;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+  const int i = tid & 7, q = tid >> 3;
+  float4 o[R];
+#pragma unroll
+  for (int x = 0; x < R; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(R == 4 ? 2 : 8)
   for (int k = 0; k < n; ++k) {
-    const float4 v =
-        p.part_o[(((long long)(c + k) * 2 + (k == 0)) * (H / 4) + q) * p.part_rows + row];
-    const float wt = wts[i][k];
-    if (wt != 0.f) {
-      o.x += wt * v.x;
-      o.y += wt * v.y;
-      o.z += wt * v.z;
-      o.w += wt * v.w;
+    const float4* src = p.part_o + (((long long)(c + k) * 2 + (k == 0)) * (H / 4) + q) * p.part_rows;
+    float4 v[R];
+#pragma unroll
+    for (int x = 0; x < R; ++x)
+      v[x] = row0 + 8 * x + i < p.part_rows ? src[row0 + 8 * x + i] : make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      const float wt = wts[8 * x + i][k];
+      if (wt != 0.f) {
+        o[x].x += wt * v[x].x;
+        o[x].y += wt * v[x].y;
+        o[x].z += wt * v[x].z;
+        o[x].w += wt * v[x].w;
+      }
     }
   }
-  const float inv = sums[i];
-  const long long at = (long long)(rec.row0 + tok) * p.hq + rec.g * p.G + r % p.G;
-  *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * H + 4 * q) =
-      make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+#pragma unroll
+  for (int x = 0; x < R; ++x) {
+    const float inv = sums[8 * x + i];
+    const long long at = row_at(row0 + 8 * x + i);
+    if (at >= 0)
+      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * H + 4 * q) =
+          make_uint2(pack2<T>(o[x].x * inv, o[x].y * inv), pack2<T>(o[x].z * inv, o[x].w * inv));
+  }
 }
 
 }  // namespace dg

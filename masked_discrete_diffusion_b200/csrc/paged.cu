@@ -219,10 +219,12 @@ dg_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const C
   DG_TRY(launch_status(launch_pdl(paged_attn_kernel<T, H>, dim3(PA_CTAS), dim3(PA_THREADS),
                                   PagedCfg<H>::SMEM, st, 1, mq, mk, mv, p),
                        "dg_paged_attention"));
-  return launch_status(
-      launch_pdl(paged_merge_kernel<T, H>, dim3(PA_CTAS, (p.part_rows + PM_ROWS - 1) / PM_ROWS),
-                 dim3(PM_ROWS * H / 4), 0, st, 1, p),
-      "dg_paged_attention (merge)");
+  const int rows = p.max_q > p.T ? 32 : 8;  // of a merge block
+  const dim3 grid(PA_CTAS, (p.part_rows + rows - 1) / rows), block(2 * H);
+  return launch_status(rows == 32
+                           ? launch_pdl(paged_merge_kernel<T, H, 4>, grid, block, 0, st, 1, p)
+                           : launch_pdl(paged_merge_kernel<T, H, 1>, grid, block, 0, st, 1, p),
+                       "dg_paged_attention (merge)");
 }
 
 }  // namespace
