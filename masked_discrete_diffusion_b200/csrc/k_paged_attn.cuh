@@ -49,7 +49,7 @@ template <int H> struct PagedCfg {
   static constexpr uint32_t TILE = CH * PA_CHUNK;   // a Q, K or V tile
   static constexpr int SLOTS = H == 128 ? 4 : 8;
   static constexpr size_t SMEM =
-      1024 + (2 + SLOTS) * TILE + 512 /* barriers, plan */ + 2 * 128 * 8 /* m, l */ +
+      1024 + (2 + SLOTS) * TILE + 768 /* barriers, plan */ + 2 * 128 * 8 /* m, l */ +
       8 * 2048 /* output staging */;
 };
 
@@ -122,10 +122,10 @@ __device__ __forceinline__ PagedKeys paged_keys(const PagedAttnParams& p, const 
 // Line length of the sequence of each lane (0 items: 0), and the extremes of its items'
 // tiles.  A lane adds up its own items when they are few or alike; longer causal chunks are
 // added up by the whole warp, one at a time.
-__device__ __forceinline__ long long paged_work(const PagedAttnParams& p, const PagedSeq& s,
-                                                int lane, int* n_min, int* n_max) {
+__device__ __forceinline__ int paged_work(const PagedAttnParams& p, const PagedSeq& s, int lane,
+                                          int* n_min, int* n_max) {
   const int step = 2 * p.T, items = (s.ql + step - 1) / step;
-  long long w = 0;
+  int w = 0;
   const bool many = items > 4 && s.causal;
   const int alone = many ? 0 : s.causal ? items : min(items, 1);
 #pragma unroll 1
@@ -145,7 +145,7 @@ __device__ __forceinline__ long long paged_work(const PagedAttnParams& p, const 
     x.kv = __shfl_sync(0xffffffffu, s.kv, src);
     x.causal = 1;
     const int items_x = (x.ql + step - 1) / step;
-    long long v = 0;
+    int v = 0;
 #pragma unroll 1
     for (int i = lane; i < items_x; i += 32) {
       const int n = paged_keys(p, x, i * step, min(step, x.ql - i * step)).n;
@@ -153,43 +153,39 @@ __device__ __forceinline__ long long paged_work(const PagedAttnParams& p, const 
       *n_max = max(*n_max, n);
       v += n + PA_ITEM;
     }
-    v = warp_sum(v);
+    v = __reduce_add_sync(0xffffffffu, v);
     if (lane == src) w = v;
   }
   return w * p.hkv;
 }
 
 // The line's division: `parts` parts in whole multiples of `unit` tiles, the first `rem` of
-// them one multiple longer.
+// them one multiple longer.  (The host refuses calls whose line could reach 2^31.)
 struct PagedSplit {
-  unsigned long long q, rem;
-  unsigned unit;
+  unsigned q, rem, unit;
   int parts;
   // total 0: no parts.  n_min, n_max: the extremes of the items' tiles.
-  __device__ __forceinline__ PagedSplit(unsigned long long total, int n_min, int n_max) {
-    unsigned long long count = total;
+  __device__ __forceinline__ PagedSplit(unsigned total, int n_min, int n_max) {
+    unsigned count = total;
     unit = 1;
-    const unsigned long long least = (total + PA_PART - 1) / PA_PART;
-    parts = (int)min((unsigned long long)PA_CTAS, least);
+    parts = (int)min((unsigned)PA_CTAS, (total + PA_PART - 1) / PA_PART);
     if (n_min == n_max && total > 0) {
-      const unsigned len = n_min + PA_ITEM;
-      const unsigned long long items = total / len;
-      const unsigned long long whole = (items + PA_CTAS - 1) / PA_CTAS * len;
-      if (whole <= total / parts + PA_MERGE) {
+      const unsigned len = n_min + PA_ITEM, items = total / len;
+      if ((items + PA_CTAS - 1) / PA_CTAS * len <= total / parts + PA_MERGE) {
         unit = len;
         count = items;
-        parts = (int)min((unsigned long long)PA_CTAS, items);
+        parts = (int)min((unsigned)PA_CTAS, items);
       }
     }
     q = count / max(parts, 1);
     rem = count - q * parts;
   }
-  __device__ __forceinline__ long long start(unsigned c) const {
-    return (long long)((c * q + min((unsigned long long)c, rem)) * unit);
+  __device__ __forceinline__ int start(unsigned c) const {
+    return (int)((c * q + min(c, rem)) * unit);
   }
-  __device__ __forceinline__ int owner(unsigned long long at) const {  // the part that holds it
+  __device__ __forceinline__ int owner(unsigned at) const {  // the part that holds it
     at /= unit;
-    const unsigned long long cut = rem * (q + 1);
+    const unsigned cut = rem * (q + 1);
     return (int)(at < cut ? at / (q + 1) : rem + (at - cut) / q);
   }
 };
@@ -207,7 +203,7 @@ struct PagedWalk {
   int i0, nt;    // the item's tokens
   int g;         // its key head
   int off;       // line units of it that lie before
-  long long left;
+  int left;      // line units of the part still to come
   // the current piece: key tiles first .. first + count - 1 of the item
   int first, count;
 
@@ -215,38 +211,35 @@ struct PagedWalk {
     nt = min(2 * p.T, s.ql - i0);
     k = paged_keys(p, s, i0, nt);
   }
-  // `count` units from unit `skip` of sequence b on (a whole warp: 32 items at a time).
-  __device__ __forceinline__ void start(const PagedAttnParams& p, int b, long long skip,
-                                        long long count_, int lane) {
+  // `count` units from unit `skip` of sequence `seq` on (a whole warp: 32 items at a time).
+  __device__ __forceinline__ void start(const PagedAttnParams& p, const PagedSeq& seq, int skip,
+                                        int count_, int lane) {
     left = count_;
     if (left <= 0) return;
-    paged_seq(p, b, &s);
+    s = seq;
     const int step = 2 * p.T, items = (s.ql + step - 1) / step;
     int at = 0;
 #pragma unroll 1
     for (int i = 0; i < items; i += 32) {
       const int mine = i + lane;
-      long long len = 0;
+      int incl = 0;
       if (mine < items)
-        len = (long long)(paged_keys(p, s, mine * step, min(step, s.ql - mine * step)).n +
-                          PA_ITEM) * p.hkv;
-      long long incl = len;
+        incl = (paged_keys(p, s, mine * step, min(step, s.ql - mine * step)).n + PA_ITEM) * p.hkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      const unsigned before = __ballot_sync(0xffffffffu, mine < items && incl <= skip);
-      const int n = __popc(before);
+      const int n = __popc(__ballot_sync(0xffffffffu, mine < items && incl <= skip));
       at = min(i + n, items - 1);
       if (n > 0) skip -= __shfl_sync(0xffffffffu, incl, n - 1);
       if (n < 32) break;
     }
     i0 = at * step;
     item(p);
-    const unsigned long long len = k.n + PA_ITEM;
-    g = (int)min((unsigned long long)skip / len, (unsigned long long)p.hkv - 1);
-    off = (int)min((unsigned long long)skip - g * len, len - 1);
+    const int len = k.n + PA_ITEM;
+    g = min((int)((unsigned)skip / (unsigned)len), p.hkv - 1);
+    off = min(skip - g * len, len - 1);
   }
   // Prepares the next piece; false at the end of the part.
   __device__ __forceinline__ bool next(const PagedAttnParams& p) {
@@ -269,7 +262,7 @@ struct PagedWalk {
           item(p);
         }
       }
-      const int take = (int)min((long long)(k.n + PA_ITEM - off), left);
+      const int take = min(k.n + PA_ITEM - off, left);
       first = paged_cut(off, k.n);
       off += take;
       left -= take;
@@ -448,10 +441,10 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
 }
 
 struct PagedPlan {
-  long long total, skip;  // tiles of the line; tiles of sequence b before this CTA's part
-  int b, n_min, n_max;
+  int sums[16], mins[16], maxs[16];  // of each warp's sequences
+  PagedSeq seq;                      // where this CTA's part begins,
+  int skip;                          // and the line units of it that lie before
   int32_t gave_up;
-  long long sums[PA_THREADS / 32];
   int32_t bad[8];  // a page out of range, by piece modulo 8
 };
 
@@ -460,61 +453,67 @@ struct PagedBars {
   uint64_t s_full[2], p_full[4] /* [stream][keys 0-63, 64-127] */, o_full[2];
   uint64_t full[8], empty[8];
 };
-static_assert(sizeof(PagedPlan) + sizeof(PagedBars) <= 512, "fits the tail of shared memory");
+static_assert(sizeof(PagedPlan) + sizeof(PagedBars) <= 768, "fits the tail of shared memory");
 
-// Fills plan.total, the extremes of the items' tiles, and plan.b / plan.skip, where the part of
-// CTA c begins (if it has one).  Every thread of the CTA calls it; a barrier must follow.
-__device__ __forceinline__ void paged_plan(const PagedAttnParams& p, PagedPlan* plan, int c) {
+// The line's division, and plan.seq / plan.skip, where the part of CTA c begins (if it has
+// one).  Every thread of the CTA calls it; a barrier must follow.  Short on purpose: each CTA
+// runs it once, and its instructions arrive as it goes.
+__device__ __forceinline__ PagedSplit paged_plan(const PagedAttnParams& p, PagedPlan* plan,
+                                                 int c) {
+  constexpr int WARPS = PA_THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long base = 0, mine = 0, incl = 0, start = 0;
+  const int chunks = (p.B + PA_THREADS - 1) / PA_THREADS;
+  PagedSeq s = {};
+  int total = 0, low = 0x7fffffff, high = 0, start = 0;
+  int mine = 0, incl = 0;
+  PagedSplit split(0, 0, 0);
+  // once to add up, once to find the part: up to a sequence a thread, the first pass's sums
+  // serve the second
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 1) {
-      if (tid == 0) plan->total = base;
-      const PagedSplit split(base, plan->n_min, plan->n_max);
-      if (c >= split.parts) return;
+  for (int i = 0; i < 2 * chunks; ++i) {
+    if (i == chunks) {
+      split = PagedSplit(total, low, high);
+      if (c >= split.parts) break;
       start = split.start(c);
-      base = 0;
+      total = 0;
     }
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += PA_THREADS) {
-      const int b = b0 + tid;
-      if (pass == 0 || p.B > PA_THREADS) {  // up to one sequence a thread: once is enough
-        PagedSeq s = {};
-        if (b < p.B && paged_seq(p, b, &s) && pass == 0 && c == 0 && p.err)
-          atomicOr(p.err, DG_PAGED_BAD_BATCH);
-        int n_min = 0x7fffffff, n_max = 0;
-        mine = paged_work(p, s, lane, &n_min, &n_max);
-        n_min = __reduce_min_sync(0xffffffffu, n_min);
-        n_max = __reduce_max_sync(0xffffffffu, n_max);
-        incl = mine;
+    if (i == 0 || chunks > 1) {
+      const int b = (i < chunks ? i : i - chunks) * PA_THREADS + tid;
+      s.ql = 0;
+      s.causal = 0;
+      if (b < p.B && paged_seq(p, b, &s) && i < chunks && c == 0 && p.err)
+        atomicOr(p.err, DG_PAGED_BAD_BATCH);
+      int n_min = 0x7fffffff, n_max = 0;
+      incl = mine = paged_work(p, s, lane, &n_min, &n_max);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        __syncthreads();
-        if (lane == 31) {
-          plan->sums[warp] = incl;
-          if (n_max > 0) {
-            atomicMin(&plan->n_min, n_min);
-            atomicMax(&plan->n_max, n_max);
-          }
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int w = 0; w < warp; ++w) incl += plan->sums[w];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
       }
-      long long all = 0;
-#pragma unroll 1
-      for (int w = 0; w < PA_THREADS / 32; ++w) all += plan->sums[w];
-      if (pass == 1 && start >= base + incl - mine && start < base + incl) {
-        plan->b = b;
-        plan->skip = start - (base + incl - mine);
+      n_min = __reduce_min_sync(0xffffffffu, n_min);
+      n_max = __reduce_max_sync(0xffffffffu, n_max);
+      if (i > 0) __syncthreads();  // the last chunk's sums have been read
+      if (lane == 31) {
+        plan->sums[warp] = incl;
+        plan->mins[warp] = n_min;
+        plan->maxs[warp] = n_max;
       }
-      base += all;
+      __syncthreads();
     }
+    const bool in = lane < WARPS;
+    int before = in ? plan->sums[lane] : 0;
+    low = min(low, __reduce_min_sync(0xffffffffu, in ? plan->mins[lane] : 0x7fffffff));
+    high = max(high, __reduce_max_sync(0xffffffffu, in ? plan->maxs[lane] : 0));
+    const int all = __reduce_add_sync(0xffffffffu, before);
+    before = __reduce_add_sync(0xffffffffu, lane < warp ? before : 0);
+    const int at = total + before + incl - mine;
+    if (i >= chunks && start >= at && start < at + mine) {
+      plan->seq = s;
+      plan->skip = start - at;
+    }
+    total += all;
   }
+  return split;
 }
 
 template <int N> __device__ __forceinline__ void reg_inc() {
@@ -541,7 +540,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   uint8_t* ring = sq + 2 * Cfg::TILE;       // SLOTS key or value tiles
   PagedBars* bar = reinterpret_cast<PagedBars*>(ring + Cfg::SLOTS * Cfg::TILE);
   PagedPlan* plan = reinterpret_cast<PagedPlan*>(bar + 1);
-  float2* xml = reinterpret_cast<float2*>(ring + Cfg::SLOTS * Cfg::TILE + 512);  // [2][128]
+  float2* xml = reinterpret_cast<float2*>(ring + Cfg::SLOTS * Cfg::TILE + 768);  // [2][128]
   uint4* stage = reinterpret_cast<uint4*>(xml + 256) + (threadIdx.x >> 5) * 128;  // 2 KB a warp
   __shared__ uint32_t tslot;
 
@@ -562,9 +561,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     }
     tc::fence_mbar_init();
     plan->gave_up = 0;
-    plan->total = 0;
-    plan->n_min = 0x7fffffff;
-    plan->n_max = 0;
     for (int i = 0; i < 8; ++i) plan->bad[i] = 0;
   }
   if (warp == 8) tc::tmem_alloc(&tslot, 512);
@@ -575,8 +571,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   }
   pdl_enter();
   const int c = blockIdx.x;
-  __syncthreads();  // the plan's initial values
-  paged_plan(p, plan, c);
+  const PagedSplit split = paged_plan(p, plan, c);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -584,11 +579,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   volatile int32_t* gave_up = &plan->gave_up;
 
   if (tid == 0) p.rec[c].valid = 0;
-  const PagedSplit split(plan->total, plan->n_min, plan->n_max);
   const bool idle = c >= split.parts;
   PagedWalk w;
-  w.start(p, idle ? 0 : plan->b, idle ? 0 : plan->skip,
-          idle ? 0 : split.start(c + 1) - split.start(c), lane);
+  w.start(p, plan->seq, plan->skip, idle ? 0 : split.start(c + 1) - split.start(c), lane);
   bool ok = true;
 
   if (warp >= 8) {
@@ -982,10 +975,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       if (tid == 0 && begins && !ends) {
         // the line's position of the item's end gives the last CTA that holds a piece
-        const long long begin = split.start(c + 1) - w.left - w.off;
+        const int begin = split.start(c + 1) - w.left - w.off;
         const int len = w.k.n + PA_ITEM;
         int last = split.owner(begin + len - 1);
-        while (last > c && paged_cut((int)(split.start(last) - begin), w.k.n) == w.k.n) --last;
+        while (last > c && paged_cut(split.start(last) - begin, w.k.n) == w.k.n) --last;
         PagedRec rec;
         rec.valid = 1;
         rec.last = last;

@@ -398,6 +398,13 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
   DG_REQUIRE((n <= 1 || q->token_stride >= 8) && (q->n_heads == 1 || q->head_stride >= 8),
              "q: strides of 0");
   if (n == 0 || batch->B == 0 || batch->max_q == 0) return DG_OK;
+  const int tokens = 2 * (128 / group);  // of an item
+  const long long items = ((n + tokens - 1) / tokens + (long long)batch->B) * cache->n_kv_heads;
+  const long long tiles = (long long)batch->max_pages * cache->page_size / PA_KT + 1 + PA_ITEM;
+  if (items >= 0x7fffffffLL / tiles) {
+    set_error("paged attention over %lld items of up to %lld key tiles: too many", items, tiles);
+    return DG_ERR_UNSUPPORTED;
+  }
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   DG_TRY(encoder(&enc));
   PagedAttnParams p{};
