@@ -23,7 +23,7 @@
 // CTA.  Warps 0-3 and 4-7: the streams' softmax, a thread a row (TMEM lane = row).  Warp 8:
 // MMA issue for both streams in turn, which keeps one's softmax under the other's products
 // (with a warp for each the streams fell into step, 5,100 cycles a pair of tiles).
-// Warp 9: TMA.  S (128 columns) and O of both streams fill TMEM; P takes S's
+// Warp 9: TMA.  Warp 10: waits for tiles on the MMA warp's behalf.  S (128 columns) and O of both streams fill TMEM; P takes S's
 // place as the A operand of O += P V.  K and V tiles pass through one ring of slots in the
 // order of their first use.  O is rescaled only when a row's maximum has grown by 2^8, by
 // its own warp; until then P's exponents are taken against the older maximum, which the
@@ -36,7 +36,7 @@
 namespace dg {
 
 constexpr int PA_CTAS = 148;
-constexpr int PA_THREADS = 384;  // 12 warps: 8 softmax, MMA, TMA, 2 that only help to plan
+constexpr int PA_THREADS = 384;  // 12 warps: 8 softmax, MMA, TMA, tile watch, one idle
 constexpr int PA_KT = 128;                 // keys a tile
 constexpr int PA_ITEM = 2;                 // an item's fixed cost in tiles
 constexpr int PA_CUT = 2;                  // no cut leaves fewer tiles on a side
@@ -410,26 +410,6 @@ __device__ __forceinline__ unsigned shl(unsigned x, unsigned n) {
   return y;
 }
 
-// Two fp32 values in a register pair, for the packed instructions.
-__device__ __forceinline__ uint64_t f2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unf2(uint64_t v, float* a, float* b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2<bf16>(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -516,6 +496,16 @@ __device__ __forceinline__ PagedSplit paged_plan(const PagedAttnParams& p, Paged
   return split;
 }
 
+// Ring places, from a piece's first, of step u's keys and values (see the MMA warp): the ring
+// holds K0 V0 K1 V1 .. for a pair, whose steps 2 i and 2 i + 1 share tile i, and
+// K0 K1 V0 K2 V1 K3 .. else.
+__device__ __forceinline__ uint32_t paged_k_at(uint32_t base, bool pair, int u) {
+  return base + (pair ? u & ~1 : u < 2 ? u : 2 * u - 1);
+}
+__device__ __forceinline__ uint32_t paged_v_at(uint32_t base, bool pair, int u, int steps) {
+  return base + (pair ? u | 1 : min(steps, 2) + u + min(u, max(steps - 2, 0)));
+}
+
 template <int N> __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
@@ -551,7 +541,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     tc::mbar_init(&bar->done, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar->s_full + i, 1);
-      tc::mbar_init(bar->p_full + 2 * i, 4);
+      tc::mbar_init(bar->p_full + 2 * i, 5);  // 4 softmax warps, and the tiles are there
       tc::mbar_init(bar->p_full + 2 * i + 1, 4);
       tc::mbar_init(bar->o_full + i, 1);
     }
@@ -678,60 +668,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     auto wait = [&](uint64_t* b, uint32_t parity) {
       ok = ok && tc::mbar_wait_or(b, parity, gave_up);
     };
-    // values nobody sees become 0, so that 0 * value is 0 whatever the slot held
-    auto clear_v = [&](uint32_t i, int lo, int hi) {
-      uint8_t* v = ring + (i % Cfg::SLOTS) * Cfg::TILE;
-#pragma unroll 1
-      for (int ch = 0; ch < Cfg::CH; ++ch) {
-        uint8_t* vc = v + ch * PA_CHUNK;
-#pragma unroll 1
-        for (int x = lane; x < lo * 8; x += 32)
-          *reinterpret_cast<uint4*>(vc + x * 16) = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-        for (int x = hi * 8 + lane; x < PA_KT * 8; x += 32)
-          *reinterpret_cast<uint4*>(vc + x * 16) = make_uint4(0, 0, 0, 0);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-    };
     for (; w.next(p); ++piece) {
       // through a reduction, whose result the compiler knows to be the same in every lane
       const bool pair = __reduce_max_sync(0xffffffffu, (unsigned)w.pair(p)) != 0;
       const int count = __reduce_max_sync(0xffffffffu, w.count);
-      const int key0 = __reduce_max_sync(0xffffffffu, (w.k.t0 + w.first) * PA_KT);
-      const int klo = __reduce_max_sync(0xffffffffu, w.k.lo) - key0;
-      const int khi = __reduce_max_sync(0xffffffffu, w.k.hi) - key0;
       const int steps = pair ? 2 * count : count;
       wait(&bar->q_full, piece & 1);
       // Step u adds P V of stream u & 1 and issues the same stream's next scores, two steps
       // ahead.  Solo: step u is key tile u.  Pair: steps 2 i and 2 i + 1 are key tile i.
-      // The ring holds K0 V0 K1 V1 .. for a pair and K0 K1 V0 K2 V1 K3 .. else.
-      uint32_t vs = 0, ks = 0;
-      uint64_t vd = 0, kd = 0;
-      // key tiles of the piece that hold keys nobody sees: the first, the last or none
-      const int cut_lo = klo > 0 ? 0 : -1, cut_hi = khi < count * PA_KT ? count - 1 : -1;
+      // The first half of P comes with the step's tiles (the next warp's doing).
 #pragma unroll 1
       for (int u = -2; u < steps; ++u) {
         const int t = u & 1;
         const bool more = u + 2 < steps;
-        // the tiles first: their waits are over long before the softmax's
-        if (!pair || t == 0) {
-          if (u >= 0) {
-            vs = base + (pair ? u + 1 : min(steps, 2) + u + min(u, max(steps - 2, 0)));
-            vd = v_desc + (uint64_t)((vs % Cfg::SLOTS) * (Cfg::TILE >> 4));
-            wait(bar->full + vs % Cfg::SLOTS, (vs / Cfg::SLOTS) & 1);
-            const int tile = pair ? u >> 1 : u;
-            if (tile == cut_lo || tile == cut_hi) {
-              const int lo = min(max(klo - tile * PA_KT, 0), PA_KT);
-              clear_v(vs, lo, min(max(khi - tile * PA_KT, lo), PA_KT));
-            }
-          }
-          if (more) {
-            ks = base + (pair ? u + 2 : u < 0 ? u + 2 : 2 * u + 3);
-            kd = k_desc + (uint64_t)((ks % Cfg::SLOTS) * (Cfg::TILE >> 4));
-            wait(bar->full + ks % Cfg::SLOTS, (ks / Cfg::SLOTS) & 1);
-          }
-        }
+        const uint32_t vs = paged_v_at(base, pair, u, steps), ks = paged_k_at(base, pair, u + 2);
+        const uint64_t vd = v_desc + (uint64_t)((vs % Cfg::SLOTS) * (Cfg::TILE >> 4));
+        const uint64_t kd = k_desc + (uint64_t)((ks % Cfg::SLOTS) * (Cfg::TILE >> 4));
+        if (u < 0 && more) wait(bar->full + ks % Cfg::SLOTS, (ks / Cfg::SLOTS) & 1);
         if (u >= 0) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {  // O_t += P_t V, 64 keys at a time
@@ -775,6 +728,59 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       if (!tc::mbar_wait(&bar->done, 0)) *gave_up = 1;
     }
     __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------ tiles for the MMA
+    // Waits for the tiles of each step on the MMA warp's behalf, whose own waits would keep
+    // the tensor cores idle (650 of 3,600 cycles a pair of tiles), and clears what no row
+    // sees in them.
+    uint32_t base = 0, said = 0;  // ring tiles of earlier pieces, parity of each stream's steps
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      ok = ok && tc::mbar_wait_or(b, parity, gave_up);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    // values nobody sees become 0, so that 0 * value is 0 whatever the slot held
+    auto clear_v = [&](uint32_t i, int lo, int hi) {
+      uint8_t* v = ring + (i % Cfg::SLOTS) * Cfg::TILE;
+#pragma unroll 1
+      for (int ch = 0; ch < Cfg::CH; ++ch) {
+        uint8_t* vc = v + ch * PA_CHUNK;
+#pragma unroll 1
+        for (int x = lane; x < lo * 8; x += 32)
+          *reinterpret_cast<uint4*>(vc + x * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int x = hi * 8 + lane; x < PA_KT * 8; x += 32)
+          *reinterpret_cast<uint4*>(vc + x * 16) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    };
+    while (w.next(p)) {
+      const bool pair = w.pair(p);
+      const int count = w.count, steps = pair ? 2 * count : count;
+      const int key0 = (w.k.t0 + w.first) * PA_KT;
+      // keys nobody sees are in the piece's first tile, its last or none
+      const int cut_lo = w.k.lo > key0 ? 0 : -1;
+      const int cut_hi = w.k.hi < key0 + count * PA_KT ? count - 1 : -1;
+#pragma unroll 1
+      for (int u = 0; u < steps; ++u) {
+        if (!pair || !(u & 1)) {
+          const uint32_t vs = paged_v_at(base, pair, u, steps), ks = paged_k_at(base, pair, u + 2);
+          const int tile = pair ? u >> 1 : u;
+          wait(bar->full + vs % Cfg::SLOTS, (vs / Cfg::SLOTS) & 1);
+          if (ok && (tile == cut_lo || tile == cut_hi)) {
+            const int lo = min(max(w.k.lo - key0 - tile * PA_KT, 0), PA_KT);
+            clear_v(vs, lo, min(max(w.k.hi - key0 - tile * PA_KT, lo), PA_KT));
+          }
+          if (u + 2 < steps) wait(bar->full + ks % Cfg::SLOTS, (ks / Cfg::SLOTS) & 1);
+        }
+        // not before the stream's last phase is over: this arrival must not count in it
+        const int t = u & 1;
+        wait(bar->p_full + 2 * t, (said >> t & 1) ^ 1);
+        said ^= 1u << t;
+        if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
+      }
+      base += 2 * count;
+    }
   }
   } else {
     // ------------------------------------------------------------------ softmax
@@ -860,7 +866,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
               float e0, e1;
-              unf2(fma2(f2(s[64 * hf + 2 * q], s[64 * hf + 2 * q + 1]), sl2, neg2), &e0, &e1);
+              const uint64_t x = fma2(f2(s[64 * hf + 2 * q], s[64 * hf + 2 * q + 1]), sl2, neg2);
+              unf2(x, &e0, &e1);
               e0 = ex2(e0);
               e1 = ex2(e1);
               sum2[q & 1] = add2(sum2[q & 1], f2(e0, e1));

@@ -33,7 +33,7 @@ struct RowsParams {
   int parts;            // warps per row
   HeadsDev q, k, v, qo, ko;  // ko: dg_qk_norm_rope only
   const void *qg, *kg;
-  float eps;            // < 0: no norm
+  float eps, inv_h;     // eps < 0: no norm; 1 / h
   int rotate;
   const int32_t* positions;  // dg_qk_norm_rope
   // append
@@ -47,6 +47,57 @@ struct RowsParams {
 __device__ __forceinline__ float widen(__half x) { return __half2float(x); }
 template <> __device__ __forceinline__ __half narrow<__half>(float x) {
   return __float2half_rn(x);
+}
+
+// Two fp32 values in a register pair, for the packed instructions.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Eight consecutive elements as four fp32 pairs, and back.
+template <class T> __device__ __forceinline__ void widen8(const T (&x)[8], uint64_t (&y)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = f2(widen(x[2 * i]), widen(x[2 * i + 1]));
+}
+__device__ __forceinline__ void narrow8(const uint64_t (&y)[4], float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unf2(y[i], &x[2 * i], &x[2 * i + 1]);
+}
+__device__ __forceinline__ void narrow8(const uint64_t (&y)[4], bf16 (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unf2(y[i], &a, &b);
+    reinterpret_cast<__nv_bfloat162*>(x)[i] = __floats2bfloat162_rn(a, b);
+  }
+}
+__device__ __forceinline__ void narrow8(const uint64_t (&y)[4], __half (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unf2(y[i], &a, &b);
+    reinterpret_cast<__half2*>(x)[i] = __floats2half2_rn(a, b);
+  }
 }
 
 // The sequence of row t: how many of q_start[1 .. B] are <= t, by a 32-way search of the
@@ -64,17 +115,40 @@ __device__ __forceinline__ int find_seq(const int32_t* q_start, int B, int t, in
   return lo + __popc(__ballot_sync(0xffffffffu, i <= hi && q_start[i] <= t));
 }
 
+constexpr int HEAD_ROWS_WARPS = 4;
+
 template <class T, bool APPEND>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(HEAD_ROWS_WARPS * 32)
     head_rows_kernel(const RowsParams p, const __grid_constant__ dg_rope rope) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(w / p.parts), part = (int)(w % p.parts);
+  const unsigned w = blockIdx.x * HEAD_ROWS_WARPS + (threadIdx.x >> 5);  // < 2^32
+  const int t = (int)(w / (unsigned)p.parts), part = (int)(w % (unsigned)p.parts);
   if (t >= p.n) return;  // warp-uniform
   const int l = lane & ((1 << p.lg) - 1);
   const int half = p.h >> 1;
   const bool on = 8 * l < half;  // lanes of a head beyond h/16 idle
+
+  const int per = 32 >> p.lg;
+  const int heads = p.hq + (APPEND ? 2 : 1) * p.hkv;
+  const int hl = lane >> p.lg;
+  // this lane's part of head j0 + hl: which of q, k, v it is (0, 1, 2) and its index there
+  auto kind_of = [&](int j) { return j < p.hq ? 0 : (!APPEND || j < p.hq + p.hkv) ? 1 : 2; };
+  auto index_of = [&](int j, int kind) {
+    return kind == 0 ? j : kind == 1 ? j - p.hq : j - p.hq - p.hkv;
+  };
+  auto load = [&](int it, T(&a)[8], T(&c)[8]) {
+    const int j = (part * p.iters + it) * per + hl;
+    if (!on || j >= heads || it >= p.iters) return;
+    const int kind = kind_of(j);
+    const HeadsDev& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+    const T* x = reinterpret_cast<const T*>(src.p + t * src.ts + index_of(j, kind) * src.hs);
+    ld8(x + 8 * l, a);
+    ld8(x + half + 8 * l, c);
+  };
+  // the rows are on their way while the row's place and its sines are worked out
+  T a[8], c[8];
+  load(0, a, c);
 
   long long pos;
   long long slot = -1;  // byte offset of the row's slot, -1: not stored
@@ -100,34 +174,47 @@ __global__ void __launch_bounds__(256)
     pos = p.rotate ? p.positions[t] : 0;
   }
 
-  float cs[8], sn[8];
+  // Sines of this lane's eight pairs.  The lanes at the same place of the warp's heads need
+  // the same eight: each works out 8 / per of them (one at least), and they exchange.
+  uint64_t cs[4], sn[4], ns[4];  // cosines, sines and their negatives
   if (p.rotate) {
+    const int each = max(8 / per, 1);  // 1, 2 or 4
+    float c4[4], s4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= each) break;
+      const int pair = 8 * l + (hl * each + i & 7);
+      // through memory: a constant-bank read of 32 different words would be 32 reads
+      unsigned long long f;
+      asm("ld.u64 %0, [%1];" : "=l"(f) : "l"(&rope.turns[on ? pair : 0]));
+      const unsigned long long turn = (unsigned long long)pos * f;
+      sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f /* 2^-31 */, &s4[i], &c4[i]);
+    }
+    float c8[8], s8[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const unsigned long long turn =
-          on ? (unsigned long long)pos * rope.turns[8 * l + i] : 0ull;
-      sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f /* 2^-31 */, &sn[i], &cs[i]);
+      const int from = (i / each << p.lg) | l;
+      const float s0 = each == 1 ? s4[0] : each == 2 ? s4[i & 1] : s4[i & 3];
+      const float c0 = each == 1 ? c4[0] : each == 2 ? c4[i & 1] : c4[i & 3];
+      s8[i] = __shfl_sync(0xffffffffu, s0, from);
+      c8[i] = __shfl_sync(0xffffffffu, c0, from);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cs[i] = f2(c8[2 * i], c8[2 * i + 1]);
+      sn[i] = f2(s8[2 * i], s8[2 * i + 1]);
+      ns[i] = f2(-s8[2 * i], -s8[2 * i + 1]);
     }
   }
 
-  const int per = 32 >> p.lg;
-  const int heads = p.hq + (APPEND ? 2 : 1) * p.hkv;
-  const int hl = lane >> p.lg;
   for (int it = 0; it < p.iters; ++it) {
     const int j0 = (part * p.iters + it) * per;
     if (j0 >= heads) break;
     const int j = j0 + hl;
-    // which of q, k, v this head is (0, 1, 2) and its index there
-    const int kind = j < p.hq ? 0 : (!APPEND || j < p.hq + p.hkv) ? 1 : 2;
-    const int jj = kind == 0 ? j : kind == 1 ? j - p.hq : j - p.hq - p.hkv;
+    const int kind = kind_of(j), jj = index_of(j, kind);
     const bool act = on && j < heads && (!APPEND || kind == 0 || slot >= 0);
-    const HeadsDev& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-    T a[8], c[8];
-    if (act) {
-      const T* x = reinterpret_cast<const T*>(src.p + t * src.ts + jj * src.hs);
-      ld8(x + 8 * l, a);
-      ld8(x + half + 8 * l, c);
-    }
+    T a2[8], c2[8];
+    load(it + 1, a2, c2);
     T* dst = nullptr;
     if (act) {
       char* base;
@@ -140,56 +227,65 @@ __global__ void __launch_bounds__(256)
       dst = reinterpret_cast<T*>(base);
     }
     if (kind != 2) {
-      float u[8], w2[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        u[i] = act ? widen(a[i]) : 0.f;
-        w2[i] = act ? widen(c[i]) : 0.f;
-      }
+      uint64_t u[4], v[4];  // the two halves' channels
+      widen8(a, u);
+      widen8(c, v);
       if (p.eps >= 0.f) {
-        float ss = 0.f;
+        uint64_t s2 = mul2(u[0], u[0]), s3 = mul2(v[0], v[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss += u[i] * u[i] + w2[i] * w2[i];
+        for (int i = 1; i < 4; ++i) {
+          s2 = fma2(u[i], u[i], s2);
+          s3 = fma2(v[i], v[i], s3);
+        }
+        float x, y;
+        unf2(add2(s2, s3), &x, &y);
+        float ss = act ? x + y : 0.f;  // idle lanes hold nothing
         // a warp's heads may be of different kinds, so each reduces within its own lanes
         // (at most 16: h <= 256)
         const unsigned m = ((1u << (1 << p.lg)) - 1u) << (hl << p.lg);
         for (int o = 1 << p.lg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(m, ss, o);
-        const float r = 1.0f / sqrtf(ss / (float)p.h + p.eps);
+        const float r = rsqrtf(ss * p.inv_h + p.eps);
+        const uint64_t r2 = f2(r, r);
         const T* gain = reinterpret_cast<const T*>(kind == 0 ? p.qg : p.kg);
-        if (gain && act) {
+        if (gain && on) {
           T g0[8], g1[8];
           ld8(gain + 8 * l, g0);
           ld8(gain + half + 8 * l, g1);
+          uint64_t e[4], f[4];
+          widen8(g0, e);
+          widen8(g1, f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            u[i] *= r * widen(g0[i]);
-            w2[i] *= r * widen(g1[i]);
+          for (int i = 0; i < 4; ++i) {
+            u[i] = mul2(u[i], mul2(r2, e[i]));
+            v[i] = mul2(v[i], mul2(r2, f[i]));
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            u[i] *= r;
-            w2[i] *= r;
+          for (int i = 0; i < 4; ++i) {
+            u[i] = mul2(u[i], r2);
+            v[i] = mul2(v[i], r2);
           }
         }
       }
       if (p.rotate) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x0 = u[i], x1 = w2[i];
-          u[i] = x0 * cs[i] - x1 * sn[i];
-          w2[i] = x1 * cs[i] + x0 * sn[i];
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t x = u[i];
+          u[i] = fma2(x, cs[i], mul2(v[i], ns[i]));
+          v[i] = fma2(v[i], cs[i], mul2(x, sn[i]));
         }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] = narrow<T>(u[i]);
-        c[i] = narrow<T>(w2[i]);
-      }
+      narrow8(u, a);
+      narrow8(v, c);
     }
     if (act) {
       st8(dst + 8 * l, a);
       st8(dst + half + 8 * l, c);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = a2[i];
+      c[i] = c2[i];
     }
   }
 }

@@ -143,15 +143,16 @@ dg_status launch_rows(RowsParams& p, const dg_rope* rope, cudaStream_t st, const
   while (p.iters < groups && (long long)p.n * ((groups + p.iters - 1) / p.iters) > 148 * 32)
     ++p.iters;
   p.parts = (groups + p.iters - 1) / p.iters;
-  const long long blocks = ((long long)p.n * p.parts + 7) / 8;
-  DG_REQUIRE(blocks <= 0x7fffffffLL, "too many rows");
+  p.inv_h = 1.0f / (float)p.h;
+  const long long blocks = ((long long)p.n * p.parts + HEAD_ROWS_WARPS - 1) / HEAD_ROWS_WARPS;
+  DG_REQUIRE(blocks * HEAD_ROWS_WARPS <= 0xffffffffLL, "too many rows");
   dg_rope r;
   if (rope)
     r = *rope;
   else
     r.head_dim = 0;
-  return launch_status(launch_pdl(head_rows_kernel<T, APPEND>, dim3((unsigned)blocks), dim3(256),
-                                  0, st, 1, p, r),
+  return launch_status(launch_pdl(head_rows_kernel<T, APPEND>, dim3((unsigned)blocks),
+                                  dim3(HEAD_ROWS_WARPS * 32), 0, st, 1, p, r),
                        what);
 }
 
