@@ -138,7 +138,7 @@ dg_status launch_rows(RowsParams& p, const dg_rope* rope, cudaStream_t st, const
   p.lg = 0;
   while ((1 << p.lg) < p.h / 16) ++p.lg;
   const int per = 32 >> p.lg;
-  const int groups = (p.hq + (APPEND ? 2 : 1) * p.hkv + per - 1) / per;
+  const int groups = (p.hq + per - 1) / per + (APPEND ? 2 : 1) * ((p.hkv + per - 1) / per);
   p.iters = 1;
   while (p.iters < groups && (long long)p.n * ((groups + p.iters - 1) / p.iters) > 148 * 32)
     ++p.iters;
