@@ -40,7 +40,7 @@ constexpr int PA_THREADS = 384;  // 12 warps: 8 softmax, MMA, TMA, tile watch, o
 constexpr int PA_KT = 128;                 // keys a tile
 constexpr int PA_ITEM = 2;                 // an item's fixed cost in tiles
 constexpr int PA_CUT = 2;                  // no cut leaves fewer tiles on a side
-constexpr int PA_PART = 5;                 // shortest part of the line
+constexpr int PA_PART = 3;                 // shortest part of the line
 constexpr int PA_MERGE = 5;                // what cutting items costs a call, in tiles
 constexpr uint32_t PA_CHUNK = 128 * 128;   // 128 rows of 64 channels
 
