@@ -654,14 +654,14 @@ def _heads(t, name: str, dtypes, dev: int, n=None, h=None) -> dg_heads:
     return dg_heads(t.data_ptr(), st[0], st[1], heads)
 
 
-def _vec(t, name: str, dtype, dev: int, n: int):
-    """Device pointer of a contiguous [n] tensor, or None."""
+def _full(t, name: str, dtype, dev: int, shape: tuple):
+    """Device pointer of a contiguous tensor of exactly this type and shape, or None."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 1 and t.shape[0] == n
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == dev and t.is_contiguous()):
         return t.data_ptr()
-    return _arg(t, name, dtype, (n,))
+    return _arg(t, name, dtype, shape)
 
 
 def _dev() -> int:
@@ -678,12 +678,24 @@ def _raw_stream(stream, dev: int):
     return torch._C._cuda_getCurrentRawStream(dev) or None
 
 
-def _like(stream, t, shape=None):
-    """An empty contiguous tensor of t's type whose memory belongs to the call's stream."""
+def _like(stream, t):
+    """An empty contiguous tensor of t's type and shape whose memory belongs to the call's
+    stream, and its dg_heads."""
     if stream is None:
-        return t.new_empty(t.shape if shape is None else shape)
+        x = torch.empty_like(t, memory_format=torch.contiguous_format)
+    else:
+        with torch.cuda.stream(stream):
+            x = torch.empty_like(t, memory_format=torch.contiguous_format)
+    _, heads, h = t.shape
+    return x, dg_heads(x.data_ptr(), heads * h, h, heads)
+
+
+def _bytes(stream, n: int, device):
+    """n bytes of scratch memory of the call's stream."""
+    if stream is None:
+        return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
-        return t.new_empty(t.shape if shape is None else shape)
+        return torch.empty_strided((n,), (1,), dtype=torch.uint8, device=device)
 
 
 class PagedCache:
@@ -727,9 +739,20 @@ class PagedBatch:
         self.B, self.max_q, self.max_pages = B, int(max_q), width
         self._p = (q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr())
         self.dev = page_table.get_device()
+        self._scratch = {}
 
     def c(self, n_tokens: int) -> dg_paged_batch:
         return dg_paged_batch(self.B, n_tokens, self.max_q, self.max_pages, *self._p)
+
+    def scratch(self, cache: PagedCache, c: dg_paged_batch, hq: int) -> int:
+        """Workspace bytes of an attention call: a function of max_q and these sizes alone."""
+        key = (hq, cache.n_kv_heads, cache.head_dim)
+        if key not in self._scratch:
+            need = ctypes.c_size_t()
+            _check(lib().dg_paged_attention_workspace(ctypes.byref(cache.c), ctypes.byref(c), hq,
+                                                      ctypes.byref(need)))
+            self._scratch[key] = need.value
+        return self._scratch[key]
 
 
 def dg_rope_init(base: float, head_dim: int) -> dg_rope:
@@ -764,15 +787,17 @@ def dg_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions=None, rope: dg_r
     dt = q.dtype
     kh = _heads(k, "k", (dt,), dev, n, h)
     if q_out is None:
-        q_out = _like(stream, q)
+        q_out, qo = _like(stream, q)
+    else:
+        qo = _heads(q_out, "q_out", (dt,), dev, n, h)
     if k_out is None:
-        k_out = _like(stream, k)
-    qo = _heads(q_out, "q_out", (dt,), dev, n, h)
-    ko = _heads(k_out, "k_out", (dt,), dev, n, h)
+        k_out, ko = _like(stream, k)
+    else:
+        ko = _heads(k_out, "k_out", (dt,), dev, n, h)
     _check(lib().dg_qk_norm_rope(
         _ELEMS[dt], n, h, ctypes.byref(qh), ctypes.byref(kh),
-        _vec(positions, "positions", torch.int32, dev, n), _opt_ref(rope),
-        _vec(q_gain, "q_gain", dt, dev, h), _vec(k_gain, "k_gain", dt, dev, h), _eps(eps),
+        _full(positions, "positions", torch.int32, dev, (n,)), _opt_ref(rope),
+        _full(q_gain, "q_gain", dt, dev, (h,)), _full(k_gain, "k_gain", dt, dev, (h,)), _eps(eps),
         ctypes.byref(qo), ctypes.byref(ko), _raw_stream(stream, dev)))
     return q_out, k_out
 
@@ -800,14 +825,14 @@ def dg_paged_append(cache: PagedCache, batch: PagedBatch, k: torch.Tensor, v: to
     if q is not None:
         qh = _heads(q, "q", dts, dev, n, h)
         if q_out is None:
-            q_out = _like(stream, q)
-    if q_out is not None:
+            q_out, qo = _like(stream, q)
+    if q_out is not None and qo is None:
         qo = _heads(q_out, "q_out", dts, dev, n, h)
     b = batch.c(n)
     _check(lib().dg_paged_append(
         ctypes.byref(cache.c), ctypes.byref(b), ctypes.byref(kh), ctypes.byref(vh),
-        _opt_ref(rope), _vec(k_gain, "k_gain", dt, dev, h), _eps(eps), _opt_ref(qh),
-        _vec(q_gain, "q_gain", dt, dev, h), _opt_ref(qo), _vec(err, "err", torch.int32, dev, 1),
+        _opt_ref(rope), _full(k_gain, "k_gain", dt, dev, (h,)), _eps(eps), _opt_ref(qh),
+        _full(q_gain, "q_gain", dt, dev, (h,)), _opt_ref(qo), _full(err, "err", torch.int32, dev, (1,)),
         _raw_stream(stream, dev)))
     return q_out
 
@@ -826,19 +851,17 @@ def dg_paged_attention(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, ca
     n, hq, _ = q.shape
     flags = None
     if isinstance(causal, torch.Tensor):
-        flags, causal = _vec(causal, "causal", torch.uint8, dev, batch.B), True
+        flags, causal = _full(causal, "causal", torch.uint8, dev, (batch.B,)), True
     b = batch.c(n)
-    need = ctypes.c_size_t()
-    _check(lib().dg_paged_attention_workspace(ctypes.byref(cache.c), ctypes.byref(b), hq,
-                                              ctypes.byref(need)))
+    need = batch.scratch(cache, b, hq)
     if out is None:
-        out = _like(stream, q, (n, hq, h))
-    ws = _like(stream, q, (need.value + 1 >> 1,))
+        out, _ = _like(stream, q)
+    ws = _bytes(stream, need, q.device)
     _check(lib().dg_paged_attention(
         ctypes.byref(cache.c), ctypes.byref(b), ctypes.byref(qh), 1 if causal else 0, flags,
-        window, h ** -0.5 if scale is None else scale, _arg(out, "out", dt, (n, hq, h)),
-        _arg(lse, "lse", torch.float32, (n, hq)), ws.data_ptr(), ws.numel() * 2,
-        _vec(err, "err", torch.int32, dev, 1), _raw_stream(stream, dev)))
+        window, h ** -0.5 if scale is None else scale, _full(out, "out", dt, dev, (n, hq, h)),
+        _full(lse, "lse", torch.float32, dev, (n, hq)), ws.data_ptr(), need,
+        _full(err, "err", torch.int32, dev, (1,)), _raw_stream(stream, dev)))
     return out
 
 
