@@ -430,7 +430,7 @@ struct PagedPlan {
 
 struct PagedBars {
   uint64_t q_full, q_empty, done;
-  uint64_t s_full[2], p_full[4] /* [stream][keys 0-63, 64-127] */, o_full[2];
+  uint64_t s_full[2], p_full[4] /* [stream][keys 0-63, 64-127] */, o_full[2], half_done[2];
   uint64_t full[8], empty[8];
 };
 static_assert(sizeof(PagedPlan) + sizeof(PagedBars) <= 768, "fits the tail of shared memory");
@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       tc::mbar_init(bar->p_full + 2 * i, 5);  // 4 softmax warps, and the tiles are there
       tc::mbar_init(bar->p_full + 2 * i + 1, 4);
       tc::mbar_init(bar->o_full + i, 1);
+      tc::mbar_init(bar->half_done + i, 1);
     }
     for (int i = 0; i < Cfg::SLOTS; ++i) {
       tc::mbar_init(bar->full + i, 1);
@@ -695,6 +696,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
               for (int k = 4 * hf; k < 4 * hf + 4; ++k)
                 tc::mma_ts(tmem + 256 + t * H, tmem + t * 128 + k * 8, vd + k * (2048 >> 4), idO,
                            u >= 2 || k != 0);
+              if (hf == 0) tc::mma_commit(bar->half_done + t);
             }
             __syncwarp();
           }
@@ -835,83 +837,79 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             }
             tc::tmem_wait_st();
           }
-          // Twice over the scores, 64 at a time and the next 32 on their way: keeping all 128
-          // in registers would save a read of TMEM (133 cycles of ~2,400) but unrolls to
-          // more code than the instruction cache next to the issue slots holds (24 blocks
-          // of 256 rows: 87 us against 81).
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto largest = [&](const float* x) {
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!(y & 1)) mx[y >> 1 & 3] = max3(mx[y >> 1 & 3], x[y], x[y + 1]);
-          };
-          float sa[32], sb[32];
-          tc::tmem_ld32_async(ts, sa);
-#pragma unroll 1
-          for (int q = 0; q < 4; q += 2) {
-            tc::tmem_wait32(sa);
-            tc::tmem_ld32_async(ts + 32 * q + 32, sb);
-            largest(sa);
-            tc::tmem_wait32(sb);
-            tc::tmem_ld32_async(ts + (32 * q + 64 & 127), sa);  // the first again after the last
-            largest(sb);
-          }
-          const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl;
-          const bool grow = mt > m + 8.f;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? mt : m;
-            const float a = grow ? ex2(m - mn) : 1.f;
-            l *= a;
-            m = mn;
-            if (i > 0) {
-#pragma unroll 1
-              for (int q = 0; q < H; q += 32) {
-                float o[32];
-                tc::tmem_ld32_async(to + q, o);
-                tc::tmem_wait32(o);
-                uint32_t ou[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) ou[x] = __float_as_uint(o[x] * a);
-                tc::tmem_st32(to + q, ou);
-              }
-            }
-          }
-          const float neg = m == -INFINITY ? 0.f : -m;
-          const uint64_t sl2 = f2(sl, sl), neg2 = f2(neg, neg);
-          uint64_t sum2[2] = {0, 0};
-          uint32_t pk[32];
-          auto weights = [&](const float* x, uint32_t* w16) {
-#pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              float e0, e1;
-              unf2(fma2(f2(x[2 * y], x[2 * y + 1]), sl2, neg2), &e0, &e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum2[y & 1] = add2(sum2[y & 1], f2(e0, e1));
-              w16[y] = pack2<T>(e0, e1);
-            }
-          };
+          // 64 keys at a time, P V of the first half under the softmax of the second.  The
+          // weights are taken against the row's old reference m at once, while the half's
+          // maximum comes out of the same pass; only where it exceeds m by 8 (the first tile,
+          // seldom later) does the reference move, O and l follow, and the half is done
+          // again.  A pass for the maximum first would lie on the way from the scores to the
+          // products (450 of 3,450 cycles a pair of tiles).
+          const uint64_t sl2 = f2(sl, sl);
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {
-            tc::tmem_wait32(sa);
-            tc::tmem_ld32_async(ts + 64 * hf + 32, sb);
-            weights(sa, pk);
-            tc::tmem_wait32(sb);
-            if (hf == 0) tc::tmem_ld32_async(ts + 64, sa);
-            weights(sb, pk + 16);
+            uint32_t pk[32];
+            float sum;
+#pragma unroll 1
+            while (true) {
+              const float neg = m == -INFINITY ? 0.f : -m;
+              const uint64_t neg2 = f2(neg, neg);
+              uint64_t sum2[2] = {0, 0};
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              auto weights = [&](const float* x, uint32_t* w16) {
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                  float e0, e1;
+                  mx[y & 3] = max3(mx[y & 3], x[2 * y], x[2 * y + 1]);
+                  unf2(fma2(f2(x[2 * y], x[2 * y + 1]), sl2, neg2), &e0, &e1);
+                  e0 = ex2(e0);
+                  e1 = ex2(e1);
+                  sum2[y & 1] = add2(sum2[y & 1], f2(e0, e1));
+                  w16[y] = pack2<T>(e0, e1);
+                }
+              };
+              float sa[32], sb[32];
+              tc::tmem_ld32_async(ts + 64 * hf, sa);
+              tc::tmem_wait32(sa);
+              tc::tmem_ld32_async(ts + 64 * hf + 32, sb);
+              weights(sa, pk);
+              tc::tmem_wait32(sb);
+              weights(sb, pk + 16);
+              float x, y;
+              unf2(add2(sum2[0], sum2[1]), &x, &y);
+              sum = x + y;
+              const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl;
+              const bool grow = mt > m + 8.f;
+              if (!__any_sync(0xffffffffu, grow)) break;
+              const float a = grow ? ex2(m - mt) : 1.f;
+              l *= a;
+              m = grow ? mt : m;
+              if (hf == 1) {  // O must have the first half's products before it is scaled
+                ok = ok && tc::mbar_wait_or(bar->half_done + t, (sc & 1) ^ 1, gave_up);
+                ok = __all_sync(0xffffffffu, ok);
+                tc::fence_after_sync();
+              }
+              if (i > 0 || hf == 1) {
+#pragma unroll 1
+                for (int q = 0; q < H; q += 32) {
+                  float o[32];
+                  tc::tmem_ld32_async(to + q, o);
+                  tc::tmem_wait32(o);
+                  uint32_t ou[32];
+#pragma unroll
+                  for (int z = 0; z < 32; ++z) ou[z] = __float_as_uint(o[z] * a);
+                  tc::tmem_st32(to + q, ou);
+                }
+              }
+            }
+            l += sum;
             // P over scores that have been read: columns 0-31, then 32-63
             tc::tmem_st32(ts + 32 * hf, pk);
             tc::tmem_wait_st();
-            if (hf == 0) {  // P V starts on the first 64 keys
+            if (hf == 0) {
               tc::fence_before_sync();
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
             }
           }
-          float sum[4];
-          unf2(sum2[0], sum, sum + 1);
-          unf2(sum2[1], sum + 2, sum + 3);
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         } else {
           tc::fence_before_sync();
           if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
