@@ -112,8 +112,8 @@ dg_status check_batch(const dg_paged_cache* c, const dg_paged_batch* b) {
   DG_REQUIRE(b, "null batch");
   DG_REQUIRE(b->B >= 0 && b->n_tokens >= 0 && b->max_q >= 0 && b->max_pages >= 0,
              "negative batch sizes");
-  DG_REQUIRE((long long)b->max_pages * c->page_size <= 0x7fffffffLL,
-             "max_pages * page_size must stay below 2^31");
+  DG_REQUIRE((long long)b->max_pages * c->page_size <= 0x7fffff00LL,
+             "max_pages * page_size must stay 256 below 2^31");
   if (b->B > 0 && b->n_tokens > 0) {
     DG_REQUIRE(b->q_start && b->kv_len && (b->page_table || b->max_pages == 0),
                "null q_start, kv_len or page_table");
@@ -220,6 +220,15 @@ dg_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const C
   DG_TRY(launch_status(launch_pdl(paged_attn_kernel<T, H>, dim3(PA_CTAS), dim3(PA_THREADS),
                                   PagedCfg<H>::SMEM, st, 1, mq, mk, mv, p),
                        "dg_paged_attention"));
+  // An item can only be cut if it can have 2 PA_CUT key tiles: the keys its rows see are the
+  // table's at most, and with a window the window's and the item's or chunk's own, which may
+  // begin inside a tile.  Short contexts need no merge (2 us of 14).
+  long long keys = (long long)p.max_pages << p.page_log2, extra = 0;
+  if (p.window && (long long)p.window + (p.max_q > 2 * p.T ? p.max_q : 2 * p.T) < keys) {
+    keys = (long long)p.window + (p.max_q > 2 * p.T ? p.max_q : 2 * p.T);
+    extra = 1;
+  }
+  if ((keys + PA_KT - 1) / PA_KT + extra < 2 * PA_CUT) return DG_OK;
   const int rows = p.max_q > p.T ? 32 : 8;  // of a merge block
   const dim3 grid(PA_CTAS, (p.part_rows + rows - 1) / rows), block(2 * H);
   return launch_status(rows == 32

@@ -11,8 +11,10 @@ Tolerances, with u = eps/2 of the type (half a step) and f = 2^-24 (fp32's):
   it); scores are sums of h products in fp32, off by (h + 4) f of the largest sum of
   |q k| scale, S, which changes each weight by twice that, exp2 by under 4 f of itself more.
   The fp32 sum over n keys (blocks of at most 128 added in a chain, each block's values one
-  by one, and at most 2^8 rescalings) rounds at most 128 + n / 64 + 256 times, in the
-  numerator and in the denominator.
+  by one, at most 2^8 rescalings and as many pieces) rounds at most 128 + n / 64 + 256
+  times, in the numerator and in the denominator.  (A piece is added after at most 148
+  others, a tile holds two additions to the chain, and a row whose maximum moves in more
+  than 2^8 tiles has lost the earlier ones to 2^-2048.)
 """
 import math
 
@@ -319,6 +321,11 @@ ATTEND = [  # dtype, h, hq, hkv, page, order, [(chunk, total)], causal flags, wi
     (F16, 64, 12, 4, 32, "page", [(i % 5, 40 + 7 * i) for i in range(40)], "mixed", 33),
     (BF16, 128, 2, 1, 128, "page", [(1500, 1500)], C, 0),
     (BF16, 128, 2, 2, 128, "page", [(1, 100000)], C, 0),
+    (F16, 64, 2, 1, 16, "page", [(300, 100), (257, 0), (200, 201)], C, 0),  # long dead stretches
+    (BF16, 128, 128, 1, 64, "page", [(70, 200), (3, 9)], C, 40),        # items of two tokens
+    (F16, 64, 4, 1, 16, "page", [(1, 1 + i % 70) for i in range(900)], C, 0),
+    (BF16, 64, 6, 2, 16, "page", [(1 + i % 3, 20 + i) for i in range(500)], "mixed", 37),
+    (BF16, 128, 4, 2, 64, "page", [(700, 900), (1, 3000), (60, 61), (130, 2000)], "mixed", 0),
 ]
 
 
@@ -356,6 +363,25 @@ def test_attention_matches_fp64(case, sharp):
     assert torch.equal(out[rows][dead], torch.zeros_like(out[rows][dead]))
     again = binding.dg_paged_attention(pg.cache, pg.batch, q, causal_arg(mode, flags), window)
     assert torch.equal(again[rows], out[rows])  # and without the optional outputs
+
+
+@pytest.mark.parametrize("step", [0.02, 0.5, 3.0])
+@pytest.mark.parametrize("seqs,causal", [([(1, 3000)], C), ([(200, 1000), (130, 700)], C),
+                                         ([(96, 900)], B)], ids=str)
+def test_attention_when_every_tile_raises_the_maximum(seqs, causal, step):
+    """Scores that climb by `step` a position (in units of log e, up to 9,000 in all): the
+    reference moves in every tile, in both halves of it, and old weights fade to nothing."""
+    h, hq, hkv = 64, 4, 2
+    pg = Pages(seqs, hkv, h, 16, BF16)
+    q = rnd(61, pg.n, hq, h)
+    q[..., 0] = 8.0  # sqrt(h): scale q.k gains k[..., 0]
+    for b, (_, kv) in enumerate(seqs):
+        page, slot = pg.slots(b, 0, kv)
+        ramp = torch.arange(kv, device="cuda").float() * step
+        pg.k[page, slot, :, 0] = ramp.to(BF16)[:, None]
+    want, bound, _, _ = attention_fp64(pg, q, [causal] * len(seqs), 0, h ** -0.5)
+    got = binding.dg_paged_attention(pg.cache, pg.batch, q, causal)
+    check(got, want, bound, BF16)
 
 
 @pytest.mark.parametrize("rot", [float("nan"), float("inf")])
