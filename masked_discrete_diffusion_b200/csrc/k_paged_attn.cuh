@@ -40,7 +40,7 @@ constexpr int PA_THREADS = 384;  // 12 warps: 8 softmax, MMA, TMA, tile watch, o
 constexpr int PA_KT = 128;                 // keys a tile
 constexpr int PA_ITEM = 2;                 // an item's fixed cost in tiles
 constexpr int PA_CUT = 2;                  // no cut leaves fewer tiles on a side
-constexpr int PA_PART = 3;                 // shortest part of the line
+constexpr int PA_PART = 2;                 // shortest part of the line
 constexpr int PA_MERGE = 5;                // what cutting items costs a call, in tiles
 constexpr uint32_t PA_CHUNK = 128 * 128;   // 128 rows of 64 channels
 
@@ -513,11 +513,11 @@ template <int N> __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-constexpr int PA_REGS_HIGH = 208, PA_REGS_LOW = 88;
+constexpr int PA_REGS_HIGH = 192, PA_REGS_LOW = 120;
 
 // Registers: 12 warps launch with 168 a thread (64,512 in all); the softmax warpgroups,
-// which hold 128 scores each, take 208 and leave the other four warps 88
-// (256 x 208 + 128 x 88 = 64,512).
+// which hold 128 scores each, take 192 and leave the other four warps 120
+// (256 x 192 + 128 x 120 = 64,512).
 template <class T, int H>
 __global__ void __launch_bounds__(PA_THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -880,14 +880,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
               const bool grow = mt > m + 8.f;
               if (!__any_sync(0xffffffffu, grow)) break;
               const float a = grow ? ex2(m - mt) : 1.f;
+              // rows that have seen nothing yet have nothing to scale
+              const bool scale = __any_sync(0xffffffffu, grow && m != -INFINITY);
               l *= a;
               m = grow ? mt : m;
-              if (hf == 1) {  // O must have the first half's products before it is scaled
-                ok = ok && tc::mbar_wait_or(bar->half_done + t, (sc & 1) ^ 1, gave_up);
-                ok = __all_sync(0xffffffffu, ok);
-                tc::fence_after_sync();
-              }
-              if (i > 0 || hf == 1) {
+              if (scale) {
+                if (hf == 1) {  // O must have the first half's products before it is scaled
+                  ok = ok && tc::mbar_wait_or(bar->half_done + t, (sc & 1) ^ 1, gave_up);
+                  ok = __all_sync(0xffffffffu, ok);
+                  tc::fence_after_sync();
+                }
 #pragma unroll 1
                 for (int q = 0; q < H; q += 32) {
                   float o[32];
