@@ -73,6 +73,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // Eight consecutive elements as four fp32 pairs, and back.
 template <class T> __device__ __forceinline__ void widen8(const T (&x)[8], uint64_t (&y)[4]) {
@@ -115,12 +120,14 @@ __device__ __forceinline__ int find_seq(const int32_t* q_start, int B, int t, in
   return lo + __popc(__ballot_sync(0xffffffffu, i <= hi && q_start[i] <= t));
 }
 
-// Eight warps a block and 64 registers: 32 warps an SM hide the loads better than loading the
-// next heads ahead did with 72 to 110 registers (23,487 rows appended: 79 us against 82 to 126).
-constexpr int HEAD_ROWS_WARPS = 8;
+// 64 registers, so that 32 warps an SM hide the loads: loading the next heads ahead took 72 to
+// 80 and was slower (23,487 rows appended: 81 to 126 us), more warps with spills as well.
+// Blocks of two warps, which make room as soon as their own rows are done (76 us; eight warps
+// a block 78).
+constexpr int HEAD_ROWS_WARPS = 2;
 
 template <class T, bool APPEND>
-__global__ void __launch_bounds__(HEAD_ROWS_WARPS * 32, 4)
+__global__ void __launch_bounds__(HEAD_ROWS_WARPS * 32, 32 / HEAD_ROWS_WARPS)
     head_rows_kernel(const RowsParams p, const __grid_constant__ dg_rope rope) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
@@ -132,20 +139,26 @@ __global__ void __launch_bounds__(HEAD_ROWS_WARPS * 32, 4)
   const bool on = 8 * l < half;  // lanes of a head beyond h/16 idle
 
   // Groups of `per` heads: the queries', then the keys', then the values' (a group holds one
-  // kind, so what depends on it is the same for the warp).
+  // kind, so what depends on it is worked out once a kind).
   const int gq = (p.hq + per - 1) >> (5 - p.lg), gk = (p.hkv + per - 1) >> (5 - p.lg);
   const int g0 = part * p.iters, g1 = min(g0 + p.iters, gq + (APPEND ? 2 : 1) * gk);
-  auto load = [&](int g, T(&a)[8], T(&c)[8]) {
-    const HeadsDev& src = g < gq ? p.q : !APPEND || g < gq + gk ? p.k : p.v;
-    const int j = (g < gq ? g : g < gq + gk ? g - gq : g - gq - gk) * per + hl;
-    if (!on || g >= g1 || j >= (g < gq ? p.hq : p.hkv)) return;
-    const T* x = reinterpret_cast<const T*>(src.p + t * src.ts + j * src.hs);
-    ld8(x + 8 * l, a);
-    ld8(x + half + 8 * l, c);
+  int kind = g0 < gq ? 0 : g0 < gq + gk ? 1 : 2;
+  int j = (g0 - (kind == 0 ? 0 : kind == 1 ? gq : gq + gk)) * per + hl;  // this lane's head
+  const char* src;  // this lane's first channels of it
+  auto source = [&] {
+    const HeadsDev& x = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+    src = x.p + t * x.ts + j * x.hs + 8 * l * (int)sizeof(T);
   };
-  // the rows are on their way while the row's place and its sines are worked out
+  auto load = [&](T(&a)[8], T(&c)[8]) {
+    if (on && j < (kind == 0 ? p.hq : p.hkv)) {
+      ld8(reinterpret_cast<const T*>(src), a);
+      ld8(reinterpret_cast<const T*>(src) + half, c);
+    }
+  };
+  // the row is on its way while its place and its sines are worked out
   T a[8], c[8];
-  load(g0, a, c);
+  source();
+  load(a, c);
 
   long long pos;
   long long slot = -1;  // byte offset of the row's slot, -1: not stored
@@ -203,81 +216,92 @@ __global__ void __launch_bounds__(HEAD_ROWS_WARPS * 32, 4)
     }
   }
 
-  char* dst = nullptr;  // the kind's row
-  long long dst_hs = 0;
+  for (int g = g0; g < g1; ++kind, j = hl) {
+    if (g > g0) {
+      source();
+      load(a, c);
+    }
+    const int heads = kind == 0 ? p.hq : p.hkv;
+    const int end = min(g1, kind == 0 ? gq : kind == 1 ? gq + gk : gq + 2 * gk);
+    if (APPEND && kind > 0 && slot < 0) return;  // keys and values have nowhere to go
+    long long src_step, dst_step;
+    char* dst;
+    if (kind == 0) {
+      dst = p.qo.p + t * p.qo.ts;
+      dst_step = p.qo.hs;
+      src_step = p.q.hs;
+    } else if (APPEND) {
+      dst = (kind == 1 ? p.kc : p.vc) + slot;
+      dst_step = p.hs;
+      src_step = kind == 1 ? p.k.hs : p.v.hs;
+    } else {
+      dst = p.ko.p + t * p.ko.ts;
+      dst_step = p.ko.hs;
+      src_step = p.k.hs;
+    }
+    dst += j * dst_step + 8 * l * (int)sizeof(T);
+    src_step *= per;
+    dst_step *= per;
+    const T* gain = reinterpret_cast<const T*>(kind == 0 ? p.qg : p.kg) + (on ? 8 * l : 0);
+    const bool gained = kind < 2 && (kind == 0 ? p.qg : p.kg) != nullptr;
 #pragma unroll 1
-  for (int g = g0; g < g1; ++g) {
-    const int kind = g < gq ? 0 : g < gq + gk ? 1 : 2;
-    const int first = kind == 0 ? 0 : kind == 1 ? gq : gq + gk;
-    if (g == g0 || g == first) {
-      if (kind == 0) {
-        dst = p.qo.p + t * p.qo.ts;
-        dst_hs = p.qo.hs;
-      } else if (APPEND) {
-        if (slot < 0) return;  // keys and values have nowhere to go
-        dst = (kind == 1 ? p.kc : p.vc) + slot;
-        dst_hs = p.hs;
-      } else {
-        dst = p.ko.p + t * p.ko.ts;
-        dst_hs = p.ko.hs;
+    while (true) {
+      if (kind < 2) {
+        uint64_t u[4], v[4];  // the two halves' channels
+        widen8(a, u);
+        widen8(c, v);
+        if (p.eps >= 0.f) {
+          uint64_t s2 = mul2(u[0], u[0]), s3 = mul2(v[0], v[0]);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) {
+            s2 = fma2(u[i], u[i], s2);
+            s3 = fma2(v[i], v[i], s3);
+          }
+          float x, y;
+          unf2(add2(s2, s3), &x, &y);
+          float ss = on ? x + y : 0.f;  // idle lanes hold nothing
+          for (int o = 1 << p.lg >> 1; o > 0; o >>= 1)
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float r = rsqrtf(ss * p.inv_h + p.eps);
+          const uint64_t r2 = f2(r, r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            u[i] = mul2(u[i], r2);
+            v[i] = mul2(v[i], r2);
+          }
+          if (gained) {  // from L1 each time: registers held through the loop cost more
+            T g8[8];
+            uint64_t e[4];
+            ld8(gain, g8);
+            widen8(g8, e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = mul2(u[i], e[i]);
+            ld8(gain + half, g8);
+            widen8(g8, e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], e[i]);
+          }
+        }
+        if (p.rotate) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t x = u[i];
+            u[i] = sub2(mul2(x, cs[i]), mul2(v[i], sn[i]));
+            v[i] = fma2(v[i], cs[i], mul2(x, sn[i]));
+          }
+        }
+        narrow8(u, a);
+        narrow8(v, c);
       }
-    }
-    const int j = (g - first) * per + hl;
-    const bool act = on && j < (kind == 0 ? p.hq : p.hkv);
-    if (g > g0) load(g, a, c);
-    if (kind < 2) {
-      uint64_t u[4], v[4];  // the two halves' channels
-      widen8(a, u);
-      widen8(c, v);
-      if (p.eps >= 0.f) {
-        uint64_t s2 = mul2(u[0], u[0]), s3 = mul2(v[0], v[0]);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) {
-          s2 = fma2(u[i], u[i], s2);
-          s3 = fma2(v[i], v[i], s3);
-        }
-        float x, y;
-        unf2(add2(s2, s3), &x, &y);
-        float ss = on ? x + y : 0.f;  // idle lanes hold nothing
-        for (int o = 1 << p.lg >> 1; o > 0; o >>= 1)
-          ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = rsqrtf(ss * p.inv_h + p.eps);
-        const uint64_t r2 = f2(r, r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          u[i] = mul2(u[i], r2);
-          v[i] = mul2(v[i], r2);
-        }
-        const T* gain = reinterpret_cast<const T*>(kind == 0 ? p.qg : p.kg);
-        if (gain) {  // from L1 each time: 16 registers held through the loop cost more
-          const T* at = gain + (on ? 8 * l : 0);
-          T g8[8];
-          uint64_t e[4];
-          ld8(at, g8);
-          widen8(g8, e);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) u[i] = mul2(u[i], e[i]);
-          ld8(at + half, g8);
-          widen8(g8, e);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], e[i]);
-        }
+      if (on && j < heads) {
+        st8(reinterpret_cast<T*>(dst), a);
+        st8(reinterpret_cast<T*>(dst) + half, c);
       }
-      if (p.rotate) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t x = u[i], m = mul2(v[i], sn[i]);
-          u[i] = fma2(x, cs[i], m ^ 0x8000000080000000ull);  // x cos - v sin
-          v[i] = fma2(v[i], cs[i], mul2(x, sn[i]));
-        }
-      }
-      narrow8(u, a);
-      narrow8(v, c);
-    }
-    if (act) {
-      T* y = reinterpret_cast<T*>(dst + j * dst_hs);
-      st8(y + 8 * l, a);
-      st8(y + half + 8 * l, c);
+      if (++g >= end) break;
+      j += per;
+      src += src_step;
+      dst += dst_step;
+      load(a, c);
     }
   }
 }
