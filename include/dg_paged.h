@@ -40,7 +40,8 @@ typedef enum dg_paged_error {
                              max_q, or kv_len outside [0, max_pages * page_size]; the
                              sequence is skipped                                        */
   DG_PAGED_BAD_PAGE = 2,  /* a page number outside [0, n_pages) where a row is stored (it
-                             is not) or a key is read (the rows that would read it are NaN) */
+                             is not) or a key is read (the sequence's rows that see it are
+                             NaN, and neighbours of theirs computed with them may be)   */
   DG_PAGED_TIMEOUT = 4    /* a bounded device-side wait gave up; outputs are undefined  */
 } dg_paged_error;
 
@@ -110,8 +111,8 @@ dg_status dg_paged_append(const dg_paged_cache* cache, const dg_paged_batch* bat
                           const void* q_gain, const dg_heads* q_out, int32_t* err,
                           void* stream);
 
-/* Bytes of workspace a dg_paged_attention call on this cache, batch and n_q_heads needs
- * (host only; the sizes and strides are read, no device memory). */
+/* Bytes of workspace a dg_paged_attention call on this cache, batch and n_q_heads needs: a
+ * function of max_q, n_q_heads, n_kv_heads and head_dim (host only, no device memory read). */
 dg_status dg_paged_attention_workspace(const dg_paged_cache* cache, const dg_paged_batch* batch,
                                        int32_t n_q_heads, size_t* bytes);
 
@@ -130,7 +131,9 @@ dg_status dg_paged_attention_workspace(const dg_paged_cache* cache, const dg_pag
  * sequence.  workspace: 256-byte aligned, at least dg_paged_attention_workspace bytes, this
  * call's alone until it has finished; it needs no initial value.
  * Requires head_dim 64 or 128, Hq a multiple of Hkv with Hq / Hkv <= 128, scale finite and
- * > 0, window >= 0. */
+ * > 0, window >= 0, q's strides > 0 where it has more than one row or head, max_pages *
+ * page_size at least 256 below 2^31, and fewer than 2^31 key tiles of 128 in all (chunk rows
+ * by key heads, against the table's width: DG_ERR_UNSUPPORTED). */
 dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* batch,
                              const dg_heads* q, int32_t causal, const uint8_t* causal_seq,
                              int32_t window, float scale, void* out, float* lse,

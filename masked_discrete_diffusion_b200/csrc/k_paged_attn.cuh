@@ -15,19 +15,30 @@
 // Split.  All items form one line, each as long as its key tiles plus PA_ITEM (what filling
 // and emptying the pipeline for it costs, in tiles); 148 CTAs take equal contiguous parts of
 // it, so no length mix leaves SMs idle.  (Items that are all alike stay whole where that costs
-// less than cutting them: eight canvases' 128 items of 10 tiles, 47 -> UNIF us.)  A CTA's part is a run of whole items with a cut one at
-// either end; cut pieces leave (m, l, O) in the workspace and paged_merge_kernel adds an
-// item's pieces in the order of the line (the same bits every time).  Each CTA finds its
-// part from the lengths on the device: no host plan, and a captured graph follows them.
+// less than cutting them: eight canvases' 128 items of 10 tiles, 47 -> 38 us.)  A CTA's part
+// is a run of whole items with a cut one at either end; cut pieces leave (m, l, O) in the
+// workspace and paged_merge_kernel adds an item's pieces in the order of the line (the same
+// bits every time).  Each CTA finds its part from the lengths on the device: no host plan, and
+// a captured graph follows them.
 //
 // CTA.  Warps 0-3 and 4-7: the streams' softmax, a thread a row (TMEM lane = row).  Warp 8:
 // MMA issue for both streams in turn, which keeps one's softmax under the other's products
-// (with a warp for each the streams fell into step, 5,100 cycles a pair of tiles).
-// Warp 9: TMA.  Warp 10: waits for tiles on the MMA warp's behalf.  S (128 columns) and O of both streams fill TMEM; P takes S's
-// place as the A operand of O += P V.  K and V tiles pass through one ring of slots in the
-// order of their first use.  O is rescaled only when a row's maximum has grown by 2^8, by
-// its own warp; until then P's exponents are taken against the older maximum, which the
-// final division cancels.
+// (with a warp for each the streams fell into step, 5,100 cycles a pair of tiles).  Warp 9:
+// TMA.  Warp 10: waits for tiles on the MMA warp's behalf.  S (128 columns) and O of both
+// streams fill TMEM; P takes S's place as the A operand of O += P V.  K and V tiles pass
+// through one ring of slots in the order of their first use.  O is rescaled only when a row's
+// maximum has grown by 2^8, by its own warp; until then P's exponents are taken against the
+// older maximum, which the final division cancels.
+//
+// Bound.  Single tokens and drafts read each visible key and value once: memory (64 sequences
+// of up to 16,384 keys: 250 us for 1.24 GB, 4.95 TB/s, 0.75 of the measured copy rate; pages
+// of 16 tokens are 2 KB boxes).  Long chunks: a pair of tiles (128 keys of 2 x 128 rows) takes
+// the tensor cores 2,050 cycles and the SFU's exponentials as long; here it takes about 3,200,
+// since a stream's next scores need the columns its weights stand in, so that softmax and
+// products of one stream follow each other (8,192 causal tokens, 16 heads of 128: 240 us,
+// 1,150 TFLOP/s, 0.69 of the measured cuBLAS burst rate).  Short work: the first scores come
+// 9,500 cycles after the start (lengths, plan, page table, keys, and instructions that no one
+// has run yet), the last rows leave 4,000 after theirs.
 #pragma once
 
 #include "k_paged_rows.cuh"
@@ -515,9 +526,8 @@ template <int N> __device__ __forceinline__ void reg_dec() {
 
 constexpr int PA_REGS_HIGH = 192, PA_REGS_LOW = 120;
 
-// Registers: 12 warps launch with 168 a thread (64,512 in all); the softmax warpgroups,
-// which hold 128 scores each, take 192 and leave the other four warps 120
-// (256 x 192 + 128 x 120 = 64,512).
+// Registers: 12 warps launch with 168 a thread (64,512 in all); the softmax warpgroups take
+// 192 and leave the other four warps 120 (256 x 192 + 128 x 120 = 64,512): no spills.
 template <class T, int H>
 __global__ void __launch_bounds__(PA_THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,

@@ -2,6 +2,8 @@
 entry points on fake pointers, the binding on host tensors, and the rotation's constants."""
 import ctypes
 import math
+import os
+import re
 from fractions import Fraction
 
 import pytest
@@ -10,6 +12,7 @@ import torch
 from masked_discrete_diffusion_b200 import binding, build
 
 BF16, F16, F32 = 0, 1, 2
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 4096  # never dereferenced: every call below is refused
 
 
@@ -104,6 +107,12 @@ def test_attention_arguments_refused(lib):
     wide = cache(head_dim=96, page_stride=16 * 2 * 96, token_stride=2 * 96, head_stride=96)
     assert attention(lib, c=wide) == 2 and b"head_dim" in lib.dg_last_error()
     assert attention(lib, q=heads(2 * 129)) == 2 and b"128" in lib.dg_last_error()
+    # one row of q may have any stride; more need their own memory
+    for kw in (dict(token_stride=0), dict(head_stride=0)):
+        assert attention(lib, q=heads(4, **kw)) == 1 and b"strides of 0" in lib.dg_last_error()
+    # a line of key tiles that 32 bits could not count
+    huge = batch(B=1 << 20, n_tokens=1 << 30, max_q=1 << 20, max_pages=1 << 22)
+    assert attention(lib, b=huge, q=heads(4)) == 2 and b"too many" in lib.dg_last_error()
 
 
 def test_append_arguments_refused(lib):
@@ -141,6 +150,29 @@ def test_empty_calls_need_no_device(lib):
     assert lib.dg_paged_attention_workspace(ref(cache()), ref(batch()), 4, ctypes.byref(n)) == 0
     assert lib.dg_paged_attention_workspace(ref(cache()), ref(batch()), 3, ctypes.byref(n)) == 1
     assert lib.dg_paged_attention_workspace(ref(cache()), ref(batch()), 4, None) == 1
+
+
+def header_fields(name):
+    """(type, field) of a struct of dg_paged.h, in order; pointers as "*"."""
+    src = open(os.path.join(ROOT, "include", "dg_paged.h")).read()
+    body = re.search(r"typedef struct %s \{(.*?)\} %s;" % (name, name), src, re.S).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    out = []
+    for decl in body.split(";"):
+        m = re.match(r"\s*(?:const\s+)?(\w+)\s*(.+)", decl.strip(), re.S)
+        for f in m.group(2).split(",") if m else ():
+            f = f.strip()
+            out.append(("*" if f.startswith("*") else m.group(1), re.sub(r"[*\s]|\[.*", "", f)))
+    return out
+
+
+@pytest.mark.parametrize("name", ["dg_heads", "dg_rope", "dg_paged_cache", "dg_paged_batch"])
+def test_structs_match_the_header(name):
+    """Field order, names and types: one out of place would hand the library a wrong pointer."""
+    kinds = {"*": ctypes.c_void_p, "int32_t": ctypes.c_int32, "int64_t": ctypes.c_int64,
+             "uint64_t": ctypes.c_uint64 * 128}
+    want = [(f, kinds[t]) for t, f in header_fields(name)]
+    assert getattr(binding, name)._fields_ == want and len(want) >= 3
 
 
 def test_rope_constants(lib):
