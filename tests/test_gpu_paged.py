@@ -560,3 +560,69 @@ def test_cache_of_a_model_moves_into_pages():
                     <= tol).all()
     kv.close()
     model.close()
+
+
+def test_shared_prefix_pages_and_interleaved_storage():
+    """Two sequences whose tables share their first pages read them as one does; keys and
+    values may be halves of one tensor; q_out may be q's own rows."""
+    dt, hq, hkv, h, ps = BF16, 8, 2, 64, 16
+    store = rnd(71, 40, 2, ps, hkv, h)
+    cache = binding.PagedCache(store[:, 0], store[:, 1])
+    table = torch.tensor([[3, 9, 11, 30, -1], [3, 9, 20, 21, 22]], dtype=torch.int32, device="cuda")
+    kv = torch.tensor([50, 70], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda")
+    batch = binding.PagedBatch(start, kv, table, 2)
+    x = rnd(72, 3, hq + 2 * hkv, h)
+    rope = binding.dg_rope_init(1e4, h)
+    apart = x.clone()
+    want_q = binding.dg_paged_append(cache, batch, apart[:, hq:hq + hkv], apart[:, hq + hkv:],
+                                     rope, None, 1e-6, apart[:, :hq])
+    got_q = binding.dg_paged_append(cache, batch, x[:, hq:hq + hkv], x[:, hq + hkv:], rope, None,
+                                    1e-6, x[:, :hq], None, x[:, :hq])
+    assert got_q.data_ptr() == x.data_ptr() and torch.equal(got_q, want_q)
+    both = binding.dg_paged_attention(cache, batch, got_q)
+    for b in range(2):
+        one = binding.PagedBatch(start[b:b + 2] - start[b], kv[b:b + 1], table[b:b + 1], 2)
+        rows = slice(int(start[b]), int(start[b + 1]))
+        alone = binding.dg_paged_attention(cache, one, got_q[rows])
+        # the split differs with the batch, so the same keys add up in another order: each
+        # result is within half a step of sum p|v| for the weights and of itself, both at
+        # most the largest |v| (and fp32's share far below the slack of these two bounds)
+        tol = 4 * half_step(dt) * float(cache.v_pages.abs().max())
+        assert float((alone.double() - both[rows].double()).abs().max()) <= tol
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """Nothing that a capture forbids happens in the first calls (tables of entry points,
+    kernel attributes)."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = """
+import sys; sys.path[:0] = [%r, %r]
+import torch
+from masked_discrete_diffusion_b200 import binding
+import test_gpu_paged as t
+pg = t.Pages([(1, 60), (3, 61)], 2, 64, 16, torch.bfloat16)
+x = t.rnd(1, 4, 8, 64)
+rope = binding.dg_rope_init(1e4, 64)
+qo = torch.empty(4, 4, 64, dtype=torch.bfloat16, device="cuda")
+out = torch.zeros_like(qo)
+def step():
+    binding.dg_paged_append(pg.cache, pg.batch, x[:, 4:6], x[:, 6:], rope, None, 1e-6, x[:, :4],
+                            None, qo)
+    binding.dg_paged_attention(pg.cache, pg.batch, qo, out=out)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+a = out.clone()
+out.zero_()
+step()
+assert torch.equal(a, out) and bool((a != 0).any())
+""" % (os.path.dirname(here), here)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
