@@ -23,16 +23,17 @@
 //
 // CTA.  Warps 0-3 and 4-7: the streams' softmax, a thread a row (TMEM lane = row).  Warp 8:
 // MMA issue for both streams in turn, which keeps one's softmax under the other's products
-// (with a warp for each the streams fell into step, 5,100 cycles a pair of tiles).  Warp 9:
-// TMA.  Warp 10: waits for tiles on the MMA warp's behalf.  S (128 columns) and O of both
+// (with a warp for each the streams fell into step, 5,100 cycles a pair of tiles).  Warps 9
+// and 11: TMA of keys and rows, and of values.  Warp 10: waits for tiles on the MMA warp's
+// behalf.  S (128 columns) and O of both
 // streams fill TMEM; P takes S's place as the A operand of O += P V.  K and V tiles pass
 // through one ring of slots in the order of their first use.  O is rescaled only when a row's
 // maximum has grown by 2^8, by its own warp; until then P's exponents are taken against the
 // older maximum, which the final division cancels.
 //
 // Bound.  Single tokens and drafts read each visible key and value once: memory (64 sequences
-// of up to 16,384 keys: 250 us for 1.24 GB, 4.95 TB/s, 0.75 of the measured copy rate; pages
-// of 16 tokens are 2 KB boxes).  Long chunks: a pair of tiles (128 keys of 2 x 128 rows) takes
+// of up to 16,384 keys: 196 us for 1.24 GB, 6.3 TB/s, 0.96 of the measured copy rate, from
+// pages of 16 tokens, 2 KB a box).  Long chunks: a pair of tiles (128 keys of 2 x 128 rows) takes
 // the tensor cores 2,050 cycles and the SFU's exponentials as long; here it takes about 3,200,
 // since a stream's next scores need the columns its weights stand in, so that softmax and
 // products of one stream follow each other (8,192 causal tokens, 16 heads of 128: 240 us,
@@ -47,7 +48,7 @@
 namespace dg {
 
 constexpr int PA_CTAS = 148;
-constexpr int PA_THREADS = 384;  // 12 warps: 8 softmax, MMA, TMA, tile watch, one idle
+constexpr int PA_THREADS = 384;  // 12 warps: 8 softmax, MMA, keys, tile watch, values
 constexpr int PA_KT = 128;                 // keys a tile
 constexpr int PA_ITEM = 2;                 // an item's fixed cost in tiles
 constexpr int PA_CUT = 2;                  // no cut leaves fewer tiles on a side
@@ -436,7 +437,8 @@ struct PagedPlan {
   PagedSeq seq;                      // where this CTA's part begins,
   int skip;                          // and the line units of it that lie before
   int32_t gave_up;
-  int32_t bad[8];  // a page out of range, by piece modulo 8
+  int32_t bad[16];  // a page out of range, of keys and of values, by piece modulo 8
+  uint32_t issued[8], issued_q;  // loads so far into each ring slot (place + 1), of rows
 };
 
 struct PagedBars {
@@ -562,7 +564,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     }
     tc::fence_mbar_init();
     plan->gave_up = 0;
-    for (int i = 0; i < 8; ++i) plan->bad[i] = 0;
+    for (int i = 0; i < 16; ++i) plan->bad[i] = 0;
+    for (int i = 0; i < 8; ++i) plan->issued[i] = 0;
+    plan->issued_q = 0;
   }
   if (warp == 8) tc::tmem_alloc(&tslot, 512);
   if (tid == PA_THREADS - 32) {
@@ -587,13 +591,19 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 
   if (warp >= 8) {
   reg_dec<PA_REGS_LOW>();
-  if (warp == 9) {
-    // ------------------------------------------------------------------ TMA
-    uint32_t n = 0, nq = 0, piece = 0;  // tiles and row tiles requested, pieces
+  if (warp == 9 || warp == 11) {
+    // ------------------------------------------------------------------ TMA, keys and values
+    // A warp each: with pages of 16 tokens a tile is 16 boxes, and one warp's bookkeeping and
+    // issue took as long as the copies (64 caches of up to 16,384 keys: 251 us, 196 with a warp
+    // for each).
+    const bool values = warp == 11;
+    const CUtensorMap* map = values ? &mv : &mk;
+    int32_t* bad_page = plan->bad + (values ? 8 : 0);
+    uint32_t base = 0, piece = 0;  // ring tiles of earlier pieces, pieces
     const int rows = min(1 << p.page_log2, PA_KT), npg = PA_KT / rows;
     const int pg = lane & (npg - 1), ch = lane / npg;  // this lane's page of a tile, and chunk
     // Page numbers: a lane holds one of 32 consecutive ones, of two such blocks, so the table
-    // is read a block ahead of its use.  (K runs at most two tiles, 16 pages, ahead of V.)
+    // is read a block ahead of its use.
     int e0 = -1, e1 = -1, blk = 0;
     auto entries = [&](int k) {
       const long long key = ((long long)k * 32 + lane) << p.page_log2;
@@ -601,16 +611,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                  ? p.table[(long long)w.s.b * p.max_pages + k * 32 + lane]
                  : -1;
     };
-    auto load = [&](const CUtensorMap* map, int tile) {
+    auto load = [&](int tile, uint32_t n) {  // into ring place n
       const int key = tile * PA_KT + pg * rows, page = key >> p.page_log2;
       const int first = (tile * PA_KT) >> (p.page_log2 + 5);  // a tile's pages share a block
-      if (first > blk + 1) {
+      if (first > blk) {
         e0 = e1;
         e1 = entries(++blk + 1);
       }
-      const int in0 = __shfl_sync(0xffffffffu, e0, page & 31);
-      const int in1 = __shfl_sync(0xffffffffu, e1, page & 31);
-      const int id = first == blk ? in0 : in1;
+      const int id = __shfl_sync(0xffffffffu, e0, page & 31);
       const bool need = ch < Cfg::CH && key < w.k.hi && key + rows > w.k.lo;
       const bool good = need && id >= 0 && id < p.n_pages;
       const unsigned mask = __ballot_sync(0xffffffffu, good);
@@ -621,16 +629,16 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       if (!ok) return;
       if (lane == 0) {
         if (bad) {
-          plan->bad[piece & 7] = 1;
+          bad_page[piece & 7] = 1;
           if (p.err) atomicOr(p.err, DG_PAGED_BAD_PAGE);
         }
+        plan->issued[s] = n + 1;
         tc::mbar_expect_tx(bar->full + s, __popc(mask) * rows * 128);
       }
       __syncwarp();
       if (good)
         tc::tma_load_4d(ring + s * Cfg::TILE + ch * PA_CHUNK + pg * rows * 128, map, bar->full + s,
                         ch * 64, key & ((1 << p.page_log2) - 1), w.g, id);
-      ++n;
     };
     for (; w.next(p); ++piece) {
       const bool pair = w.pair(p);
@@ -638,18 +646,21 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       blk = (t0 * PA_KT) >> (p.page_log2 + 5);
       e0 = entries(blk);
       e1 = entries(blk + 1);
-      if (lane == 0) plan->bad[piece & 7] = 0;
-      // in the order of first use (the MMA warp's loop); but the first keys go before the
-      // rows, whose buffer the last piece may still hold
+      if (lane == 0) bad_page[piece & 7] = 0;
 #pragma unroll 1
-      for (int u = -2; u < steps; ++u) {
-        if (u == (piece == 0 ? -2 : 0)) {
+      for (int i = 0; i < w.count; ++i) {
+        // the rows: at once in the first piece, later after the piece's first two key tiles,
+        // since the last piece may still hold their buffer
+        if (!values && i == (piece == 0 ? 0 : min(w.count - 1, 2))) {
+          if (piece > 0 && w.count <= 2) load(t0 + i, paged_k_at(base, pair, pair ? 2 * i : i));
           ok = ok && tc::mbar_wait_or(&bar->q_empty, (piece & 1) ^ 1, gave_up);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
             const int tiles = pair ? 2 : 1;
-            ++nq;
-            if (lane == 0) tc::mbar_expect_tx(&bar->q_full, tiles * Cfg::CH * p.G * p.T * 128);
+            if (lane == 0) {
+              plan->issued_q = piece + 1;
+              tc::mbar_expect_tx(&bar->q_full, tiles * Cfg::CH * p.G * p.T * 128);
+            }
             __syncwarp();
             if (lane < tiles * Cfg::CH) {
               const int t = lane / Cfg::CH, qc = lane % Cfg::CH;
@@ -657,15 +668,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                               w.g * p.G, w.s.q0 + w.i0 + t * p.T);
             }
           }
+          if (piece > 0 && w.count <= 2) continue;
         }
-        if (pair && (u & 1)) continue;
-        if (u >= 0) load(&mv, t0 + (pair ? u >> 1 : u));
-        if (u + 2 < steps) load(&mk, t0 + (pair ? (u + 2) >> 1 : u + 2));
+        const int u = pair ? 2 * i : i;
+        load(t0 + i, values ? paged_v_at(base, pair, u, steps) : paged_k_at(base, pair, u));
       }
+      base += 2 * w.count;
     }
-    // no copy may land after the CTA has gone: normally all have been waited for already
-    if (!tc::drain_slots(bar->full, Cfg::SLOTS, (int)n)) *gave_up = 1;
-    if (nq > 0 && !tc::mbar_wait(&bar->q_full, (nq - 1) & 1)) *gave_up = 1;
   } else if (warp == 8) {
     // ------------------------------------------------------------------ MMA
     uint32_t base = 0, piece = 0;  // ring tiles of earlier pieces, pieces
@@ -936,7 +945,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
       }
       // ---- the piece's rows: whole items to out, cut ones to the workspace
-      const bool bad = plan->bad[piece & 7] != 0;
+      const bool bad = (plan->bad[piece & 7] | plan->bad[8 + (piece & 7)]) != 0;
       const bool begins = w.first == 0, ends = w.first + w.count == w.k.n;
       // this row within the item's rows of out (-1: none), and in the workspace
       const int row_at = live ? (i0 + tok) * p.hq + w.g * p.G + head : -1;
@@ -1035,7 +1044,15 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (tid == 0 && plan->gave_up && p.err) atomicOr(p.err, DG_PAGED_TIMEOUT);
+  if (tid == 0) {
+    // no copy may land after the CTA has gone: normally all have been waited for already
+    bool landed = true;
+    for (int i = 0; i < Cfg::SLOTS; ++i)
+      if (plan->issued[i])
+        landed = tc::mbar_wait(bar->full + i, ((plan->issued[i] - 1) / Cfg::SLOTS) & 1) && landed;
+    if (plan->issued_q) landed = tc::mbar_wait(&bar->q_full, (plan->issued_q - 1) & 1) && landed;
+    if ((plan->gave_up || !landed) && p.err) atomicOr(p.err, DG_PAGED_TIMEOUT);
+  }
   if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
