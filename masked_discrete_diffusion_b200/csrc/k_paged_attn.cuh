@@ -1058,81 +1058,71 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 
 // Adds the pieces of cut items: block (c, y) takes rows 8 R y .. of the item that starts and
 // does not end in CTA c.  Thread (row, 4 channels) with 8 rows fastest, so that a piece's
-// channels of 8 rows are one 128-byte line, and R such rows a thread.  R = 4 for items of
-// two row tiles: mostly two pieces, 1,184 blocks in one wave (with R = 1 four waves, 17 us
-// against 12 from a cold L2); R = 1 for one: many pieces and few blocks (drafted tokens,
-// 16 against 12 us).
+// channels of 8 rows are one 128-byte line, and R such rows a thread.  Every thread keeps its
+// rows' running maximum and sum itself: (m, l) and O of several pieces are on their way
+// together and nothing waits for another thread (weights by a first pass through shared memory
+// were half as long again).  R = 4 for items of two row tiles, mostly two pieces each; R = 1
+// for one, many pieces and few blocks.
 template <class T, int H, int R>
 __global__ void __launch_bounds__(2 * H) paged_merge_kernel(const PagedAttnParams p) {
-  constexpr int PM_ROWS = 8 * R;
-  __shared__ float wts[PM_ROWS][PA_CTAS + 1];
-  __shared__ float sums[PM_ROWS];
   pdl_enter();
-  const int c = blockIdx.x, tid = threadIdx.x;
+  const int c = blockIdx.x, i = threadIdx.x & 7, q = threadIdx.x >> 3;
   const PagedRec rec = p.rec[c];
   if (!rec.valid) return;
   const int n = min(rec.last, PA_CTAS - 1) - c + 1;
-  const int row0 = blockIdx.y * PM_ROWS;
-  auto row_at = [&](int row) -> long long {  // the row's place in out, -1: none
-    const int r = row & 127, tk = r / p.G, tok = (row >> 7) * p.T + tk;
-    if (row >= p.part_rows || tk >= p.T || tok >= rec.ntok) return -1;
-    return (long long)(rec.row0 + tok) * p.hq + rec.g * p.G + r % p.G;
-  };
-  // k-th piece: slot 1 of CTA c, then slot 0 of c + k.  Eight lanes a row.
-  for (int i = tid >> 3; i < PM_ROWS; i += H / 4) {
-    const int row = row0 + i, l8 = tid & 7;
-    const unsigned lanes = 0xffu << (tid & 24);
-    const bool in = row < p.part_rows;
-    float M = -INFINITY;
-    for (int k = l8; in && k < n; k += 8)
-      M = fmaxf(M, p.part_ml[((long long)(c + k) * 2 + (k == 0)) * p.part_rows + row].x);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, o));
-    float L = 0.f;
-    for (int k = l8; in && k < n; k += 8) {
-      const float2 ml = p.part_ml[((long long)(c + k) * 2 + (k == 0)) * p.part_rows + row];
-      const float wt = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-      wts[i][k] = wt;
-      L += ml.y != ml.y ? ml.y : wt * ml.y;  // NaN: a page out of range
-    }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(lanes, L, o);
-    if (l8 == 0) {
-      sums[i] = L == 0.f ? 0.f : 1.f / L;
-      const long long at = p.lse ? row_at(row) : -1;
-      if (at >= 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-    }
-  }
-  __syncthreads();
-  const int i = tid & 7, q = tid >> 3;
+  const int row0 = blockIdx.y * 8 * R + i;
+  constexpr int AHEAD = R == 4 ? 2 : 8;
+  float M[R], L[R];
   float4 o[R];
 #pragma unroll
-  for (int x = 0; x < R; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll(R == 4 ? 2 : 8)
-  for (int k = 0; k < n; ++k) {
-    const float4* src = p.part_o + (((long long)(c + k) * 2 + (k == 0)) * (H / 4) + q) * p.part_rows;
-    float4 v[R];
+  for (int x = 0; x < R; ++x) {
+    M[x] = -INFINITY;
+    L[x] = 0.f;
+    o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += AHEAD) {
+    float2 ml[AHEAD][R];
+    float4 v[AHEAD][R];
 #pragma unroll
-    for (int x = 0; x < R; ++x)
-      v[x] = row0 + 8 * x + i < p.part_rows ? src[row0 + 8 * x + i] : make_float4(0, 0, 0, 0);
+    for (int y = 0; y < AHEAD; ++y) {
+      // k-th piece: slot 1 of CTA c, then slot 0 of c + k.  Past the last piece or row the
+      // last again, unused: loads without branches go out together.
+      const int k = min(k0 + y, n - 1);
+      const long long at = ((long long)(c + k) * 2 + (k == 0)) * p.part_rows;
 #pragma unroll
-    for (int x = 0; x < R; ++x) {
-      const float wt = wts[8 * x + i][k];
-      if (wt != 0.f) {
-        o[x].x += wt * v[x].x;
-        o[x].y += wt * v[x].y;
-        o[x].z += wt * v[x].z;
-        o[x].w += wt * v[x].w;
+      for (int x = 0; x < R; ++x) {
+        const int row = min(row0 + 8 * x, p.part_rows - 1);
+        ml[y][x] = p.part_ml[at + row];
+        v[y][x] = p.part_o[at * (H / 4) + (long long)q * p.part_rows + row];
       }
     }
+#pragma unroll
+    for (int y = 0; y < AHEAD; ++y)
+#pragma unroll
+      for (int x = 0; x < R; ++x) {
+        if (k0 + y >= n) break;
+        const float m = ml[y][x].x, Mn = fmaxf(M[x], m);
+        const float a = M[x] == -INFINITY ? 0.f : ex2(M[x] - Mn);
+        const float b = m == -INFINITY ? 0.f : ex2(m - Mn);
+        M[x] = Mn;
+        L[x] = L[x] * a + ml[y][x].y * b;  // NaN stays NaN: a page out of range
+        o[x].x = o[x].x * a + v[y][x].x * b;
+        o[x].y = o[x].y * a + v[y][x].y * b;
+        o[x].z = o[x].z * a + v[y][x].z * b;
+        o[x].w = o[x].w * a + v[y][x].w * b;
+      }
   }
 #pragma unroll
   for (int x = 0; x < R; ++x) {
-    const float inv = sums[8 * x + i];
-    const long long at = row_at(row0 + 8 * x + i);
-    if (at >= 0)
-      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * H + 4 * q) =
-          make_uint2(pack2<T>(o[x].x * inv, o[x].y * inv), pack2<T>(o[x].z * inv, o[x].w * inv));
+    const int row = row0 + 8 * x, r = row & 127, tk = r / p.G, tok = (row >> 7) * p.T + tk;
+    if (row >= p.part_rows || tk >= p.T || tok >= rec.ntok) continue;
+    const long long at = (long long)(rec.row0 + tok) * p.hq + rec.g * p.G + (r - tk * p.G);
+    const float inv = L[x] == 0.f ? 0.f : 1.f / L[x];
+    *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at * H + 4 * q) =
+        make_uint2(pack2<T>(o[x].x * inv, o[x].y * inv), pack2<T>(o[x].z * inv, o[x].w * inv));
+    if (p.lse && q == 0)
+      p.lse[at] = L[x] == 0.f ? -INFINITY : (M[x] + log2f(L[x])) * 0.6931471805599453f;
   }
 }
 
