@@ -229,10 +229,10 @@ dg_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const C
     extra = 1;
   }
   if ((keys + PA_KT - 1) / PA_KT + extra < 2 * PA_CUT) return DG_OK;
-  const int rows = p.max_q > p.T ? 32 : 8;  // of a merge block
+  const int rows = p.max_q > p.T ? 24 : 8;  // of a merge block
   const dim3 grid(PA_CTAS, (p.part_rows + rows - 1) / rows), block(2 * H);
-  return launch_status(rows == 32
-                           ? launch_pdl(paged_merge_kernel<T, H, 4>, grid, block, 0, st, 1, p)
+  return launch_status(rows == 24
+                           ? launch_pdl(paged_merge_kernel<T, H, 3>, grid, block, 0, st, 1, p)
                            : launch_pdl(paged_merge_kernel<T, H, 1>, grid, block, 0, st, 1, p),
                        "dg_paged_attention (merge)");
 }
