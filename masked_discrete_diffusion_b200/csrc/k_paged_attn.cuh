@@ -731,12 +731,18 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
               tc::mma_bf16(tmem + t * 128, qd + o, kd + o, idS, k != 0);
             }
             tc::mma_commit(bar->s_full + t);
-            if (!pair || t == 1) tc::mma_commit(bar->empty + ks % Cfg::SLOTS);
-            if (u + 3 == steps) tc::mma_commit(&bar->q_empty);
           }
+          // The ring's places are released in their order, values (place vs) before keys (a
+          // later one).  Consecutive places of one loader lie at most 3 apart (at a piece's
+          // end), so the release that let it load place n - 3 is that of n - 7, and n - 8 is
+          // free as well: its wait for place n - 4 (4 slots) never meets the parity of n - 8.
           if (u >= 0) {
             if (!more) tc::mma_commit(bar->o_full + t);
             if (!pair || t == 1) tc::mma_commit(bar->empty + vs % Cfg::SLOTS);
+          }
+          if (more) {
+            if (!pair || t == 1) tc::mma_commit(bar->empty + ks % Cfg::SLOTS);
+            if (u + 3 == steps) tc::mma_commit(&bar->q_empty);
           }
         }
         __syncwarp();
@@ -753,7 +759,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     // ------------------------------------------------------------------ tiles for the MMA
     // Waits for the tiles of each step on the MMA warp's behalf, whose own waits would keep
     // the tensor cores idle (650 of 3,600 cycles a pair of tiles), and clears what no row
-    // sees in them.
+    // sees in them.  A slot's two latest tiles differ in parity, so a wait for a tile is sound
+    // only once the slot's previous tile has landed, and copies land in any order.  It waits
+    // for all tiles itself but a piece's first keys, which the MMA warp waits for; that those
+    // have landed it learns from the scores made of them, before any wait for the tiles that
+    // follow them in their slots.
     uint32_t base = 0, said = 0;  // ring tiles of earlier pieces, parity of each stream's steps
     auto wait = [&](uint64_t* b, uint32_t parity) {
       ok = ok && tc::mbar_wait_or(b, parity, gave_up);
@@ -784,19 +794,23 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       const int cut_hi = w.k.hi < key0 + count * PA_KT ? count - 1 : -1;
 #pragma unroll 1
       for (int u = 0; u < steps; ++u) {
-        if (!pair || !(u & 1)) {
-          const uint32_t vs = paged_v_at(base, pair, u, steps), ks = paged_k_at(base, pair, u + 2);
+        const int t = u & 1;
+        const bool tiles = !pair || t == 0;
+        if (tiles) {
+          const uint32_t vs = paged_v_at(base, pair, u, steps);
           const int tile = pair ? u >> 1 : u;
           wait(bar->full + vs % Cfg::SLOTS, (vs / Cfg::SLOTS) & 1);
           if (ok && (tile == cut_lo || tile == cut_hi)) {
             const int lo = min(max(w.k.lo - key0 - tile * PA_KT, 0), PA_KT);
             clear_v(vs, lo, min(max(w.k.hi - key0 - tile * PA_KT, lo), PA_KT));
           }
-          if (u + 2 < steps) wait(bar->full + ks % Cfg::SLOTS, (ks / Cfg::SLOTS) & 1);
         }
-        // not before the stream's last phase is over: this arrival must not count in it
-        const int t = u & 1;
-        wait(bar->p_full + 2 * t, (said >> t & 1) ^ 1);
+        // (this also keeps the arrival below out of the stream's last phase, which is over)
+        wait(bar->s_full + t, said >> t & 1);
+        if (tiles && u + 2 < steps) {
+          const uint32_t ks = paged_k_at(base, pair, u + 2);
+          wait(bar->full + ks % Cfg::SLOTS, (ks / Cfg::SLOTS) & 1);
+        }
         said ^= 1u << t;
         if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
       }

@@ -626,3 +626,25 @@ assert torch.equal(a, out) and bool((a != 0).any())
 """ % (os.path.dirname(here), here)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("q,length,causal", [(9, 20000, True), (1, 30000, True), (150, 4000, False)])
+def test_calls_in_a_row_over_scattered_pages_agree(q, length, causal):
+    """The copies of one call land in many orders when its pages lie far apart in memory that no
+    cache holds: every call's bits are the first one's, and no wait gives up."""
+    hkv, h, ps, b = 4, 128, 32, 16
+    pg = Pages([(q, length - 517 * i % 1900) for i in range(b)], hkv, h, ps, BF16, seed=81,
+               extra=5000)
+    x = rnd(83, pg.n, 8 * hkv, h)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = binding.dg_paged_attention(pg.cache, pg.batch, x, causal, err=err)
+    assert torch.isfinite(first).all()
+    out, flush = torch.empty_like(first), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(200):
+        if i % 2:
+            flush.fill_(i)
+        binding.dg_paged_attention(pg.cache, pg.batch, x, causal, out=out, err=err)
+        wrong += (out.view(torch.int16) != first.view(torch.int16)).sum()
+    assert int(wrong) == 0
+    binding.dg_paged_check(err)
