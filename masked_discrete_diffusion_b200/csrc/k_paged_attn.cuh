@@ -32,12 +32,12 @@
 // older maximum, which the final division cancels.
 //
 // Bound.  Single tokens and drafts read each visible key and value once: memory (64 sequences
-// of up to 16,384 keys: 196 us for 1.24 GB, 6.3 TB/s, 0.96 of the measured copy rate, from
+// of up to 16,384 keys: 204 us for 1.24 GB, 6.1 TB/s, 0.92 of the measured copy rate, from
 // pages of 16 tokens, 2 KB a box).  Long chunks: a pair of tiles (128 keys of 2 x 128 rows) takes
 // the tensor cores 2,050 cycles and the SFU's exponentials as long; here it takes about 3,200,
 // since a stream's next scores need the columns its weights stand in, so that softmax and
-// products of one stream follow each other (8,192 causal tokens, 16 heads of 128: 240 us,
-// 1,150 TFLOP/s, 0.69 of the measured cuBLAS burst rate).  Short work: the first scores come
+// products of one stream follow each other (8,192 causal tokens, 16 heads of 128: 240 to 253 us,
+// 1,090 to 1,150 TFLOP/s, 0.66 to 0.69 of the measured cuBLAS burst rate).  Short work: the first scores come
 // 9,500 cycles after the start (lengths, plan, page table, keys, and instructions that no one
 // has run yet), the last rows leave 4,000 after theirs.
 #pragma once
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   if (warp == 9 || warp == 11) {
     // ------------------------------------------------------------------ TMA, keys and values
     // A warp each: with pages of 16 tokens a tile is 16 boxes, and one warp's bookkeeping and
-    // issue took as long as the copies (64 caches of up to 16,384 keys: 251 us, 196 with a warp
+    // issue took as long as the copies (64 caches of up to 16,384 keys: 251 us, 204 with a warp
     // for each).
     const bool values = warp == 11;
     const CUtensorMap* map = values ? &mv : &mk;
