@@ -93,8 +93,9 @@ struct PagedSeq {
   int b, q0, ql, past, kv, causal;
 };
 
-// Sequence b, with ql = 0 where its numbers are out of range (true then).
-__device__ __forceinline__ bool paged_seq(const PagedAttnParams& p, int b, PagedSeq* s) {
+// Sequence b, with ql = 0 where its numbers are out of range: bit 0 then, and bit 1 where
+// q_start decreases (paged_plan then leaves the whole batch out).
+__device__ __forceinline__ int paged_seq(const PagedAttnParams& p, int b, PagedSeq* s) {
   const int q0 = p.q_start[b], q1 = p.q_start[b + 1], kv = p.kv_len[b];
   s->b = b;
   s->q0 = q0;
@@ -104,7 +105,7 @@ __device__ __forceinline__ bool paged_seq(const PagedAttnParams& p, int b, Paged
   s->ql = bad ? 0 : q1 - q0;
   s->past = bad ? 0 : kv - s->ql;
   s->causal = p.causal_seq ? p.causal_seq[b] != 0 : p.causal != 0;
-  return bad;
+  return (int)bad | (q1 < q0) << 1;
 }
 
 // Keys [lo, hi) that tokens i0 .. i0 + nt - 1 of the sequence see between them, and the tile
@@ -172,7 +173,8 @@ __device__ __forceinline__ int paged_work(const PagedAttnParams& p, const PagedS
 }
 
 // The line's division: `parts` parts in whole multiples of `unit` tiles, the first `rem` of
-// them one multiple longer.  (The host refuses calls whose line could reach 2^31.)
+// them one multiple longer.  (The host refuses calls whose line could reach 2^31, counting
+// each row once: chunks that do not overlap.)
 struct PagedSplit {
   unsigned q, rem, unit;
   int parts;
@@ -433,7 +435,8 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
 }
 
 struct PagedPlan {
-  int sums[16], mins[16], maxs[16];  // of each warp's sequences
+  unsigned sums[16];                 // of each warp's sequences
+  int mins[16], maxs[16];
   PagedSeq seq;                      // where this CTA's part begins,
   int skip;                          // and the line units of it that lie before
   int32_t gave_up;
@@ -450,22 +453,23 @@ static_assert(sizeof(PagedPlan) + sizeof(PagedBars) <= 768, "fits the tail of sh
 
 // The line's division, and plan.seq / plan.skip, where the part of CTA c begins (if it has
 // one).  Every thread of the CTA calls it; a barrier must follow.  Short on purpose: each CTA
-// runs it once, and its instructions arrive as it goes.
+// runs it once, and its instructions arrive as it goes.  Where q_start decreases chunks may
+// overlap, their rows would have no one owner and the line could outgrow 32 bits: no parts.
 __device__ __forceinline__ PagedSplit paged_plan(const PagedAttnParams& p, PagedPlan* plan,
                                                  int c) {
   constexpr int WARPS = PA_THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunks = (p.B + PA_THREADS - 1) / PA_THREADS;
   PagedSeq s = {};
-  int total = 0, low = 0x7fffffff, high = 0, start = 0;
-  int mine = 0, incl = 0;
+  int low = 0x7fffffff, high = 0, back = 0;
+  unsigned total = 0, start = 0, mine = 0, incl = 0;
   PagedSplit split(0, 0, 0);
   // once to add up, once to find the part: up to a sequence a thread, the first pass's sums
   // serve the second
 #pragma unroll 1
   for (int i = 0; i < 2 * chunks; ++i) {
     if (i == chunks) {
-      split = PagedSplit(total, low, high);
+      split = PagedSplit(back ? 0 : total, low, high);
       if (c >= split.parts) break;
       start = split.start(c);
       total = 0;
@@ -474,13 +478,13 @@ __device__ __forceinline__ PagedSplit paged_plan(const PagedAttnParams& p, Paged
       const int b = (i < chunks ? i : i - chunks) * PA_THREADS + tid;
       s.ql = 0;
       s.causal = 0;
-      if (b < p.B && paged_seq(p, b, &s) && i < chunks && c == 0 && p.err)
-        atomicOr(p.err, DG_PAGED_BAD_BATCH);
+      const int bad = b < p.B ? paged_seq(p, b, &s) : 0;
+      if (bad && i < chunks && c == 0 && p.err) atomicOr(p.err, DG_PAGED_BAD_BATCH);
       int n_min = 0x7fffffff, n_max = 0;
       incl = mine = paged_work(p, s, lane, &n_min, &n_max);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
       n_min = __reduce_min_sync(0xffffffffu, n_min);
@@ -491,18 +495,18 @@ __device__ __forceinline__ PagedSplit paged_plan(const PagedAttnParams& p, Paged
         plan->mins[warp] = n_min;
         plan->maxs[warp] = n_max;
       }
-      __syncthreads();
+      back |= __syncthreads_or(bad & 2);
     }
     const bool in = lane < WARPS;
-    int before = in ? plan->sums[lane] : 0;
+    unsigned before = in ? plan->sums[lane] : 0;
     low = min(low, __reduce_min_sync(0xffffffffu, in ? plan->mins[lane] : 0x7fffffff));
     high = max(high, __reduce_max_sync(0xffffffffu, in ? plan->maxs[lane] : 0));
-    const int all = __reduce_add_sync(0xffffffffu, before);
+    const unsigned all = __reduce_add_sync(0xffffffffu, before);
     before = __reduce_add_sync(0xffffffffu, lane < warp ? before : 0);
-    const int at = total + before + incl - mine;
+    const unsigned at = total + before + incl - mine;
     if (i >= chunks && start >= at && start < at + mine) {
       plan->seq = s;
-      plan->skip = start - at;
+      plan->skip = (int)(start - at);
     }
     total += all;
   }
@@ -563,6 +567,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       tc::mbar_init(bar->empty + i, 1);
     }
     tc::fence_mbar_init();
+    plan->seq = {p.B, 0, 0, 0, 0, 0};  // no sequence, should lengths that change hide the part's
+    plan->skip = 0;
     plan->gave_up = 0;
     for (int i = 0; i < 16; ++i) plan->bad[i] = 0;
     for (int i = 0; i < 8; ++i) plan->issued[i] = 0;

@@ -409,7 +409,7 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
              "q: strides of 0");
   if (n == 0 || batch->B == 0 || batch->max_q == 0) return DG_OK;
   const int tokens = 2 * (128 / group);  // of an item
-  const long long items = ((n + tokens - 1) / tokens + (long long)batch->B) * cache->n_kv_heads;
+  const long long items = ((n - 1LL) / tokens + 1 + batch->B) * cache->n_kv_heads;
   const long long tiles = (long long)batch->max_pages * cache->page_size / PA_KT + 1 + PA_ITEM;
   if (items >= 0x7fffffffLL / tiles) {
     set_error("paged attention over %lld items of up to %lld key tiles: too many", items, tiles);

@@ -1,0 +1,66 @@
+"""Paged-cache operators where their inputs are malformed or at the edge of a type: what the
+device must notice, and what must not leak into the rows beside it."""
+import pytest
+import torch
+
+from masked_discrete_diffusion_b200 import binding, build
+from test_gpu_paged import BF16, F16, Pages, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+
+
+def err_word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def guarded(rows, *shape, dt):
+    """A tensor of sevens and its middle `rows` rows."""
+    mem = torch.full((rows + 16, *shape), 7.0, dtype=dt, device="cuda")
+    return mem, mem[8:8 + rows]
+
+
+# ------------------------------------------------------------------ decreasing q_start
+@pytest.mark.parametrize("B,n", [(4, 40), (3, 300), (500, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_skips_a_batch_whose_chunks_overlap(B, n, causal):
+    """q_start = 0, n, 0, n, ..: every second sequence is in order by itself and has all rows.
+    Nothing is written, inside out and lse or beside them, and the next call is right."""
+    pg = Pages([(n, 400)] + [(0, 400)] * (B - 1), 2, 64, 64, BF16)
+    q = rnd(1, n, 8, 64)
+    want = binding.dg_paged_attention(pg.cache, pg.batch, q, causal)
+    good = pg.q_start.clone()
+    for bad in ([n * (i % 2) for i in range(B + 1)], [0] + [n] * (B - 1) + [n - 1]):
+        pg.q_start.copy_(torch.tensor(bad, dtype=torch.int32))
+        mem, out = guarded(n, 8, 64, dt=BF16)
+        lmem, lse = guarded(n, 8, dt=torch.float32)
+        err = err_word()
+        binding.dg_paged_attention(pg.cache, pg.batch, q, causal, out=out, lse=lse, err=err)
+        assert int(err) == binding.PAGED_BAD_BATCH
+        assert bool((mem == 7).all()) and bool((lmem == 7).all())
+    pg.q_start.copy_(good)
+    err = err_word()
+    assert torch.equal(binding.dg_paged_attention(pg.cache, pg.batch, q, causal, err=err), want)
+    binding.dg_paged_check(err)
+
+
+def test_attention_skips_overlapping_chunks_whose_tiles_pass_32_bits():
+    """The same with chunks and tables so long that the accepted sequences' key tiles would
+    number more than 2^31 together, while the rows counted once stay below."""
+    n, hq, hkv, h, ps = 262144, 128, 8, 64, 1024
+    k = rnd(2, 1, ps, hkv, h, dt=F16)
+    cache = binding.PagedCache(k, k.clone())
+    table = torch.zeros(4, 1024, dtype=torch.int32, device="cuda")
+    kv = torch.full((4,), 1 << 20, dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, n, 0, n, 0], dtype=torch.int32, device="cuda")
+    batch = binding.PagedBatch(start, kv, table, n)
+    q = torch.zeros(n, hq, h, dtype=F16, device="cuda")
+    out = torch.full((n, hq, h), 7.0, dtype=F16, device="cuda")
+    err = err_word()
+    binding.dg_paged_attention(cache, batch, q, False, out=out, err=err)
+    assert int(err) == binding.PAGED_BAD_BATCH
+    assert all(bool((x == 7).all()) for x in out.split(1 << 15))
