@@ -965,7 +965,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
       }
       // ---- the piece's rows: whole items to out, cut ones to the workspace
-      const bool bad = (plan->bad[piece & 7] | plan->bad[8 + (piece & 7)]) != 0;
       const bool begins = w.first == 0, ends = w.first + w.count == w.k.n;
       // this row within the item's rows of out (-1: none), and in the workspace
       const int row_at = live ? (i0 + tok) * p.hq + w.g * p.G + head : -1;
@@ -982,6 +981,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         w1 = b.x == -INFINITY ? 0.f : ex2(b.x - M);
         L = w0 * a.y + w1 * b.y;
       }
+      // Read only here: the loaders have looked at all of the piece's pages once each stream's
+      // products are done, and a stream without a tile of its own has waited for none but at
+      // the barrier above.
+      const bool bad = (plan->bad[piece & 7] | plan->bad[8 + (piece & 7)]) != 0;
       if (bad) L = __int_as_float(0x7fc00000);
       const float inv = L == 0.f ? 0.f : 1.f / L;
       const bool whole = begins && ends;

@@ -64,3 +64,26 @@ def test_attention_skips_overlapping_chunks_whose_tiles_pass_32_bits():
     binding.dg_paged_attention(cache, batch, q, False, out=out, err=err)
     assert int(err) == binding.PAGED_BAD_BATCH
     assert all(bool((x == 7).all()) for x in out.split(1 << 15))
+
+
+# ------------------------------------------------------------------ bad pages
+@pytest.mark.parametrize("dt,h", [(BF16, 128), (F16, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_bad_pages_of_single_tile_sequences_make_whole_rows_nan(dt, h, causal):
+    """Sequences of one key tile, more of them than a CTA's flags have places for: all channels
+    of a sequence with a bad page are NaN, and no other row changes a bit."""
+    shapes = [(1, 40), (1, 128), (2, 20), (20, 100), (1, 1), (3, 77)]
+    pg = Pages([shapes[i % 6] for i in range(600)], 4, h, 16, dt)
+    q = rnd(31, pg.n, 8, h, dt=dt)
+    clean = binding.dg_paged_attention(pg.cache, pg.batch, q, causal)
+    assert torch.isfinite(clean).all()
+    rotten = torch.zeros(pg.n, dtype=torch.bool, device="cuda")
+    for b in range(0, 600, 7):
+        pg.table[b, 0] = -1 if b % 2 else pg.k.shape[0]
+        rotten[pg.starts[b]:pg.starts[b + 1]] = True
+    for _ in range(20):
+        err, lse = err_word(), torch.zeros(pg.n, 8, device="cuda")
+        got = binding.dg_paged_attention(pg.cache, pg.batch, q, causal, lse=lse, err=err)
+        assert int(err) == binding.PAGED_BAD_PAGE
+        assert bool(got[rotten].isnan().all()) and bool(lse[rotten].isnan().all())
+        assert torch.equal(got[~rotten], clean[~rotten])
