@@ -126,7 +126,8 @@ dg_status dg_paged_attention_workspace(const dg_paged_cache* cache, const dg_pag
  * A row that sees nothing gets 0 and lse -inf.  lse (nullable): [n_tokens, Hq] fp32, the
  * natural log of the sum of exponentials.  out: [n_tokens, Hq, head_dim] of the cache's
  * type, contiguous, 16-byte aligned.  Scores, softmax and sums are fp32; the weights are
- * rounded to the cache's type before they meet the values.
+ * rounded to the cache's type before they meet the values (f16: by at most 2^-32 of the
+ * row's largest weight where that is more than half a step of the weight itself).
  * Keys and values at positions no row of the sequence sees, slots past kv_len included,
  * may hold anything; a non-finite value that some row sees can reach other rows of the same
  * sequence.  workspace: 256-byte aligned, at least dg_paged_attention_workspace bytes, this

@@ -29,7 +29,8 @@
 // streams fill TMEM; P takes S's place as the A operand of O += P V.  K and V tiles pass
 // through one ring of slots in the order of their first use.  O is rescaled only when a row's
 // maximum has grown by 2^8, by its own warp; until then P's exponents are taken against the
-// older maximum, which the final division cancels.
+// older maximum, which the final division cancels.  P is rounded to the cache's type, as the
+// tensor cores take it, while l adds the fp32 weights: half a step of each weight.
 //
 // Bound.  Single tokens and drafts read each visible key and value once: memory (64 sequences
 // of up to 16,384 keys: 204 us for 1.24 GB, 6.1 TB/s, 0.92 of the measured copy rate, from
@@ -423,6 +424,14 @@ __device__ __forceinline__ unsigned shl(unsigned x, unsigned n) {
   asm("shl.b32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(n));
   return y;
 }
+
+// A row's reference m is set PA_LIFT below its maximum and may lag it by 8 more: the weights
+// 2^(s - m) reach 2^8 in bf16, whose exponents have room below 1, and 2^15 in f16, whose
+// largest number is 65,504 and whose steps below 2^-14 stay at 2^-24.  Lifted by 2^7, f16
+// keeps its 11 bits down to 2^-21 of the largest weight (2^-14 else), and what it rounds off
+// of smaller ones is at most 2^-32 of the largest.  l and O carry the factor alike.
+template <class T> constexpr float PA_LIFT = 0.f;
+template <> constexpr float PA_LIFT<__half> = 7.f;
 
 template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2<bf16>(float lo, float hi) {
@@ -878,7 +887,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           }
           // 64 keys at a time, P V of the first half under the softmax of the second.  The
           // weights are taken against the row's old reference m at once, while the half's
-          // maximum comes out of the same pass; only where it exceeds m by 8 (the first tile,
+          // maximum comes out of the same pass; only where it exceeds m by far (the first tile,
           // seldom later) does the reference move, O and l follow, and the half is done
           // again.  A pass for the maximum first would lie on the way from the scores to the
           // products (450 of 3,450 cycles a pair of tiles).
@@ -916,13 +925,13 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
               unf2(add2(sum2[0], sum2[1]), &x, &y);
               sum = x + y;
               const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl;
-              const bool grow = mt > m + 8.f;
+              const bool grow = mt - m > 8.f + PA_LIFT<T>;  // (a difference: exact where it counts)
               if (!__any_sync(0xffffffffu, grow)) break;
-              const float a = grow ? ex2(m - mt) : 1.f;
+              const float a = grow ? ex2(m - (mt - PA_LIFT<T>)) : 1.f;
               // rows that have seen nothing yet have nothing to scale
               const bool scale = __any_sync(0xffffffffu, grow && m != -INFINITY);
               l *= a;
-              m = grow ? mt : m;
+              m = grow ? mt - PA_LIFT<T> : m;
               if (scale) {
                 if (hf == 1) {  // O must have the first half's products before it is scaled
                   ok = ok && tc::mbar_wait_or(bar->half_done + t, (sc & 1) ^ 1, gave_up);

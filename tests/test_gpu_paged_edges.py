@@ -87,3 +87,44 @@ def test_bad_pages_of_single_tile_sequences_make_whole_rows_nan(dt, h, causal):
         assert int(err) == binding.PAGED_BAD_PAGE
         assert bool(got[rotten].isnan().all()) and bool(lse[rotten].isnan().all())
         assert torch.equal(got[~rotten], clean[~rotten])
+
+
+# ------------------------------------------------------------------ small weights
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("h,seqs,causal", [(64, [(1, 65537), (1, 3000)], True),
+                                           (128, [(130, 20000)], False), (64, [(3, 129)], True)])
+@pytest.mark.parametrize("below", [14.25, 18.375, 21.5, 24.5, 27.25])
+def test_many_small_weights_beside_a_large_one(dt, h, seqs, causal, below):
+    """One key (an attention sink, its value 0) whose weight is 2^below times that of every
+    other key, whose values are 1.  The scores are sums of two products of few bits, so their
+    fp32 sums are exact; `below` is taken in units of log 2 by the scale.
+
+    The result is n 2^-below / (1 + n 2^-below) for n other keys.  Off by: half a step of each
+    weight and of the result (2 u of it); f16's steps, the largest weight standing at 2^7: at
+    most 2^-32 of the largest weight a key, n 2^-32 / (1 + n 2^-below) in all; the result's
+    subnormal step (2^-25 in f16); fp32's share as in the attention test, (384 + n / 64) 2^-23
+    of the result; 2^-20 for exp2 and the exponent's rounding (below 2^5: 2^-20 of a power); and
+    the scale, which is 1 / log2(e) to within three roundings: `below` 3 2^-24 of a power."""
+    hq, hkv, ps = 4, 2, 64
+    pg = Pages(seqs, hkv, h, ps, dt)
+    pg.k.zero_(), pg.v.fill_(1)
+    q = torch.zeros(pg.n, hq, h, dtype=dt, device="cuda")
+    q[..., 0] = 1
+    for b in range(len(seqs)):
+        page, slot = pg.slots(b, 5, 6)
+        pg.k[page, slot, :, 0] = below
+        pg.v[page, slot] = 0
+    scale = 0.6931471805599453
+    got = binding.dg_paged_attention(pg.cache, pg.batch, q, causal, scale=scale).double()
+    u = torch.finfo(dt).eps / 2
+    for b, (ql, kv) in enumerate(seqs):
+        rows = got[pg.starts[b]:pg.starts[b + 1]]
+        n = torch.tensor([(kv - ql + i + 1 if causal else kv) - 1 for i in range(ql)],
+                         dtype=torch.float64, device="cuda")[:, None, None]
+        mass = n * 2.0 ** -below
+        want = mass / (1 + mass)
+        tol = 2 * u * want + ((384 + n / 64) * 2.0 ** -23 + 2.0 ** -20
+                                + below * 3 * 2.0 ** -24) * want
+        if dt == F16:
+            tol = tol + n * 2.0 ** -32 / (1 + mass) + 2.0 ** -25
+        assert float(((rows - want).abs() - tol).max()) <= 0
