@@ -39,7 +39,8 @@ typedef enum dg_paged_error {
   DG_PAGED_BAD_BATCH = 1, /* q_start leaves [0, n_tokens], a chunk longer than max_q, or
                              kv_len outside [0, max_pages * page_size]: the sequence is
                              skipped.  q_start decreases: dg_paged_attention skips the whole
-                             batch, since its chunks may overlap                        */
+                             batch, since its chunks may overlap, and of what belongs to it
+                             dg_paged_append may write any part                         */
   DG_PAGED_BAD_PAGE = 2,  /* a page number outside [0, n_pages) where a row is stored (it
                              is not) or a key is read (the sequence's rows that see it are
                              NaN, and neighbours of theirs computed with them may be)   */

@@ -132,8 +132,20 @@ __global__ void __launch_bounds__(HEAD_ROWS_WARPS * 32, 32 / HEAD_ROWS_WARPS)
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const unsigned w = blockIdx.x * HEAD_ROWS_WARPS + (threadIdx.x >> 5);  // < 2^32
+  const unsigned row_warps = (unsigned)p.n * (unsigned)p.parts;
+  if (w >= row_warps) {  // warp-uniform
+    // The warps behind the rows' look at the batch, a sequence a lane: rows find their sequence
+    // by a search, which passes by chunks that are empty or out of order.
+    const unsigned b = (w - row_warps) * 32 + lane;
+    if (APPEND && p.err && b < (unsigned)p.B) {
+      const int q0 = p.q_start[b], q1 = p.q_start[b + 1], kv = p.kv_len[b];
+      if (q0 < 0 || q1 < q0 || q1 > p.n || q1 - q0 > p.max_q || kv < 0 ||
+          kv > (long long)p.max_pages << p.page_log2)
+        atomicOr(p.err, DG_PAGED_BAD_BATCH);
+    }
+    return;
+  }
   const int t = (int)(w / (unsigned)p.parts), part = (int)(w % (unsigned)p.parts);
-  if (t >= p.n) return;  // warp-uniform
   const int l = lane & ((1 << p.lg) - 1), hl = lane >> p.lg, per = 32 >> p.lg;
   const int half = p.h >> 1;
   const bool on = 8 * l < half;  // lanes of a head beyond h/16 idle
@@ -168,10 +180,8 @@ __global__ void __launch_bounds__(HEAD_ROWS_WARPS * 32, 32 / HEAD_ROWS_WARPS)
     const int q0 = p.q_start[b], q1 = p.q_start[b + 1], kv = p.kv_len[b];
     if (t < q0) return;
     if (q0 < 0 || q1 > p.n || q1 <= t || q1 - q0 > p.max_q || kv < 0 ||
-        kv > (long long)p.max_pages << p.page_log2) {
-      if (lane == 0 && p.err) atomicOr(p.err, DG_PAGED_BAD_BATCH);
+        kv > (long long)p.max_pages << p.page_log2)
       return;
-    }
     pos = (long long)kv - (q1 - q0) + (t - q0);
     if (pos >= 0) {
       const int page = p.table[(long long)b * p.max_pages + (pos >> p.page_log2)];

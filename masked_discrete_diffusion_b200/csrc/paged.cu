@@ -144,7 +144,9 @@ dg_status launch_rows(RowsParams& p, const dg_rope* rope, cudaStream_t st, const
     ++p.iters;
   p.parts = (groups + p.iters - 1) / p.iters;
   p.inv_h = 1.0f / (float)p.h;
-  const long long blocks = ((long long)p.n * p.parts + HEAD_ROWS_WARPS - 1) / HEAD_ROWS_WARPS;
+  const long long checks = APPEND && p.err ? (p.B + 31LL) / 32 : 0;  // warps
+  const long long blocks =
+      ((long long)p.n * p.parts + checks + HEAD_ROWS_WARPS - 1) / HEAD_ROWS_WARPS;
   DG_REQUIRE(blocks * HEAD_ROWS_WARPS <= 0xffffffffLL, "too many rows");
   dg_rope r;
   if (rope)

@@ -128,3 +128,33 @@ def test_many_small_weights_beside_a_large_one(dt, h, seqs, causal, below):
         if dt == F16:
             tol = tol + n * 2.0 ** -32 / (1 + mass) + 2.0 ** -25
         assert float(((rows - want).abs() - tol).max()) <= 0
+
+
+# ------------------------------------------------------------------ append's checks
+@pytest.mark.parametrize("starts,lens", [
+    ([0, 10, 5, 20], [20, 20, 20]),                  # decreasing, every chunk within max_q
+    ([0, 20, 20, 20], [20, -1, 20]),                 # an empty chunk with a negative length,
+    ([0, 20, 20, 20], [20, 20, 33]),                 # with one that its table cannot hold
+    ([0, 0, 0, 21], [0, 0, 21]),                     # rows that the call does not have
+    ([-5, -2, 0, 20], [20, 20, 20]),                 # chunks in front of the rows
+    ([0] * 100 + [7, 20] + [20] * 50, [20] * 120 + [40] + [20] * 30),
+], ids=str)
+def test_append_and_attention_flag_the_same_batches(starts, lens):
+    """Every fault of the batch sets the bit, whether or not a row meets it."""
+    B = len(lens)
+    assert len(starts) == B + 1
+    pages = rnd(41, 2 * B, 16, 2, 64)
+    cache = binding.PagedCache(pages, pages.clone())
+    table = torch.arange(2 * B, device="cuda", dtype=torch.int32).view(B, 2)
+    x = rnd(42, 20, 2, 64)
+
+    def bits(starts, lens):
+        batch = binding.PagedBatch(torch.tensor(starts, dtype=torch.int32, device="cuda"),
+                                   torch.tensor(lens, dtype=torch.int32, device="cuda"), table, 20)
+        a, b = err_word(), err_word()
+        binding.dg_paged_append(cache, batch, x, x, err=a)
+        binding.dg_paged_attention(cache, batch, x, err=b)
+        return int(a), int(b)
+
+    assert bits(starts, lens) == (binding.PAGED_BAD_BATCH, binding.PAGED_BAD_BATCH)
+    assert bits([0] * B + [20], [20] * B) == (0, 0)
