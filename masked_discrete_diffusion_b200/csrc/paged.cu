@@ -230,7 +230,7 @@ dg_status launch_attention(const CUtensorMap& mq, const CUtensorMap& mk, const C
     keys = (long long)p.window + (p.max_q > 2 * p.T ? p.max_q : 2 * p.T);
     extra = 1;
   }
-  if ((keys + PA_KT - 1) / PA_KT + extra < 2 * PA_CUT) return DG_OK;
+  if ((keys + PA_KT - 1) / PA_KT + extra < 2 * PA_CUT || p.part_rows == 0) return DG_OK;
   const int rows = p.max_q > p.T ? 24 : 8;  // of a merge block
   const dim3 grid(PA_CTAS, (p.part_rows + rows - 1) / rows), block(2 * H);
   return launch_status(rows == 24
@@ -409,7 +409,7 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
   // the tensor maps that describe q cannot repeat or overlap rows
   DG_REQUIRE((n <= 1 || q->token_stride >= 8) && (q->n_heads == 1 || q->head_stride >= 8),
              "q: strides of 0");
-  if (n == 0 || batch->B == 0 || batch->max_q == 0) return DG_OK;
+  if (n == 0 || batch->B == 0 || (batch->max_q == 0 && !err)) return DG_OK;
   const int tokens = 2 * (128 / group);  // of an item
   const long long items = ((n - 1LL) / tokens + 1 + batch->B) * cache->n_kv_heads;
   const long long tiles = (long long)batch->max_pages * cache->page_size / PA_KT + 1 + PA_ITEM;

@@ -158,3 +158,20 @@ def test_append_and_attention_flag_the_same_batches(starts, lens):
 
     assert bits(starts, lens) == (binding.PAGED_BAD_BATCH, binding.PAGED_BAD_BATCH)
     assert bits([0] * B + [20], [20] * B) == (0, 0)
+
+
+def test_chunks_beyond_a_bound_of_no_rows_are_flagged():
+    """max_q = 0: any chunk is too long for both operators; a batch of empty chunks is fine."""
+    pg = Pages([(2, 600), (0, 20)], 2, 64, 16, BF16)
+    batch = binding.PagedBatch(pg.q_start, pg.kv_len, pg.table, 0)
+    q, kv = rnd(51, 2, 4, 64), rnd(52, 2, 2, 64)
+    for want in (binding.PAGED_BAD_BATCH, 0):
+        mem, out = guarded(2, 4, 64, dt=BF16)
+        keep = pg.kmem.clone()
+        a, b = err_word(), err_word()
+        binding.dg_paged_append(pg.cache, batch, kv, kv, err=a)
+        binding.dg_paged_attention(pg.cache, batch, q, out=out, err=b)
+        binding.dg_paged_attention(pg.cache, batch, q, out=out)
+        assert (int(a), int(b)) == (want, want)
+        assert bool((mem == 7).all()) and torch.equal(pg.kmem, keep)
+        pg.q_start.zero_()
