@@ -845,6 +845,8 @@ def dg_paged_attention(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, ca
     the whole chunk).  window: the positions back a causal row sees, itself included, or
     that a bidirectional chunk sees before itself (0: all).  scale: 1 / sqrt(h) unless
     given.  lse: float32 [n, Hq] to receive the log of each row's sum of exponentials."""
+    if not -0x80000000 <= window <= 0x7fffffff:  # ctypes would cut it: 2^32 to "no limit"
+        raise ValueError("window outside [0, 2^31)")
     dev = _device_of(cache, batch)
     h, dt = cache.head_dim, cache.dtype
     qh = _heads(q, "q", cache.dtypes, dev, None, h)
