@@ -133,8 +133,8 @@ dg_status dg_paged_attention_workspace(const dg_paged_cache* cache, const dg_pag
  * may hold anything; a non-finite value that some row sees can reach other rows of the same
  * sequence.  workspace: 256-byte aligned, at least dg_paged_attention_workspace bytes, this
  * call's alone until it has finished; it needs no initial value.
- * Requires head_dim 64 or 128, Hq a multiple of Hkv with Hq / Hkv <= 128, scale finite and
- * > 0, window >= 0, q's strides > 0 where it has more than one row or head, max_pages *
+ * Requires head_dim 64 or 128, Hq a multiple of Hkv with Hq / Hkv <= 128, scale > 0 and
+ * scale log2(e) finite in fp32, window >= 0, q's strides > 0 where it has more than one row or head, max_pages *
  * page_size at least 256 below 2^31, and fewer than 2^31 key tiles of 128 in all (chunk rows
  * by key heads, against the table's width: DG_ERR_UNSUPPORTED). */
 dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* batch,

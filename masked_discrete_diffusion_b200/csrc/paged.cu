@@ -399,7 +399,9 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
   }
   DG_TRY(check_heads(q, "q", n, h, 2));
   DG_REQUIRE(window >= 0, "negative window");
-  DG_REQUIRE(std::isfinite(scale) && scale > 0.f, "scale must be finite and > 0");
+  const float scale_log2 = scale * 1.4426950408889634f;  // the kernel's: exponents of 2
+  DG_REQUIRE(std::isfinite(scale_log2) && scale > 0.f,
+             "scale must be > 0 and, times log2(e), finite");
   DG_REQUIRE(n == 0 || (out && aligned(out, 16)), "out must be 16-byte aligned and not null");
   DG_REQUIRE(aligned(lse, 4) && aligned(err, 4), "lse and err must be 4-byte aligned");
   size_t need = 0;
@@ -452,7 +454,7 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
   p.causal = causal;
   p.causal_seq = causal_seq;
   p.window = window;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.out = out;
   p.lse = lse;
   p.err = err;
