@@ -37,6 +37,12 @@ dg_status dg_op_moe(dg_model* m, int32_t layer, const float* x, float* out, int3
  * (fp32, FP8 experts). */
 dg_status dg_debug_stall_experts(dg_model* m, int64_t limit_ns);
 
+/* The same for dg_paged_attention (dg_paged.h): the next launch from the calling thread loads
+ * keys but no values, and limits every wait to limit_ns nanoseconds (1e5 .. 1e9).  The waits
+ * for values run out, the kernel unwinds and sets DG_PAGED_TIMEOUT in its err; the call's
+ * outputs are undefined, later calls run normally. */
+dg_status dg_debug_stall_paged(int64_t limit_ns);
+
 #ifdef __cplusplus
 }
 #endif

@@ -159,6 +159,7 @@ def lib() -> ctypes.CDLL:
             "dg_op_gemm": [vp, vp, vp, vp, i32, i32, i32, vp],
             "dg_op_moe": [vp, i32, vp, vp, i32, vp],
             "dg_debug_stall_experts": [vp, ctypes.c_int64],
+            "dg_debug_stall_paged": [ctypes.c_int64],
             "dg_generate_block_annealed": [vp, vp, ctypes.POINTER(dg_anneal_params), vp, vp,
                                            vp, vp],
             "dg_anneal_forward": [vp, vp, vp, i32, ctypes.POINTER(dg_anneal_params), vp, vp,
@@ -195,7 +196,7 @@ def exported_symbols():
                         "dg_anneal_forward", "dg_anneal_sample", "dg_anneal_init",
                         "dg_set_selfcond", "dg_selfcond_forward", "dg_rope_init",
                         "dg_qk_norm_rope", "dg_paged_append", "dg_paged_attention_workspace",
-                        "dg_paged_attention")
+                        "dg_paged_attention", "dg_debug_stall_paged")
             if hasattr(lib(), n)]
 
 
@@ -865,6 +866,11 @@ def dg_paged_attention(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, ca
         _full(lse, "lse", torch.float32, dev, (n, hq)), ws.data_ptr(), need,
         _full(err, "err", torch.int32, dev, (1,)), _raw_stream(stream, dev)))
     return out
+
+
+def dg_debug_stall_paged(limit_ns: int):
+    """Test hook: this thread's next dg_paged_attention launch runs its waits out after limit_ns."""
+    _check(lib().dg_debug_stall_paged(limit_ns))
 
 
 def dg_paged_check(err: torch.Tensor):

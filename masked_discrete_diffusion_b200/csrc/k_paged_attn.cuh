@@ -77,6 +77,8 @@ struct PagedAttnParams {
   void* out;
   float* lse;
   int32_t* err;
+  uint64_t wait_ns;  // limit of every wait
+  int stall;         // != 0 (tests of the way out only): no values are loaded
   // workspace
   int part_rows;  // rows of a piece
   float4* part_o;   // [PA_CTAS][2][H / 4][part_rows]: a warp's rows are contiguous
@@ -295,15 +297,18 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// mbar_wait that also gives up once another role has (and says so to the others).
+// mbar_wait that also gives up once another role has (and says so to the others).  A role
+// that has given up arrives nowhere any more: arrivals for tiles that were not waited for
+// would let the MMA warp run on and release slots whose copies never came, and the wait for
+// the copies in flight at the end of the kernel counts on each slot's phases.
 __device__ __forceinline__ bool mbar_wait_or(uint64_t* bar, uint32_t parity,
-                                             volatile int32_t* gave_up) {
+                                             volatile int32_t* gave_up, uint64_t limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*gave_up) return false;
-    if (global_ns() - t0 > 2000000000ull) {
+    if (global_ns() - t0 > limit_ns) {
       *gave_up = 1;
       return false;
     }
@@ -612,6 +617,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     // issue took as long as the copies (64 caches of up to 16,384 keys: 251 us, 204 with a warp
     // for each).
     const bool values = warp == 11;
+    ok = !values || !p.stall;
     const CUtensorMap* map = values ? &mv : &mk;
     int32_t* bad_page = plan->bad + (values ? 8 : 0);
     uint32_t base = 0, piece = 0;  // ring tiles of earlier pieces, pieces
@@ -639,7 +645,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       const unsigned mask = __ballot_sync(0xffffffffu, good);
       const bool bad = __any_sync(0xffffffffu, need && !good);
       const int s = n % Cfg::SLOTS;
-      ok = ok && tc::mbar_wait_or(bar->empty + s, ((n / Cfg::SLOTS) & 1) ^ 1, gave_up);
+      ok = ok && tc::mbar_wait_or(bar->empty + s, ((n / Cfg::SLOTS) & 1) ^ 1, gave_up, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       if (lane == 0) {
@@ -668,7 +674,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         // since the last piece may still hold their buffer
         if (!values && i == (piece == 0 ? 0 : min(w.count - 1, 2))) {
           if (piece > 0 && w.count <= 2) load(t0 + i, paged_k_at(base, pair, pair ? 2 * i : i));
-          ok = ok && tc::mbar_wait_or(&bar->q_empty, (piece & 1) ^ 1, gave_up);
+          ok = ok && tc::mbar_wait_or(&bar->q_empty, (piece & 1) ^ 1, gave_up, p.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
             const int tiles = pair ? 2 : 1;
@@ -701,7 +707,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     const uint64_t v_desc = tc::sdesc_mn128(tc::smem_addr(ring));
     // Only the elected thread's `ok` counts, so the lanes need no vote.
     auto wait = [&](uint64_t* b, uint32_t parity) {
-      ok = ok && tc::mbar_wait_or(b, parity, gave_up);
+      ok = ok && tc::mbar_wait_or(b, parity, gave_up, p.wait_ns);
     };
     for (; w.next(p); ++piece) {
       // through a reduction, whose result the compiler knows to be the same in every lane
@@ -781,7 +787,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     // follow them in their slots.
     uint32_t base = 0, said = 0;  // ring tiles of earlier pieces, parity of each stream's steps
     auto wait = [&](uint64_t* b, uint32_t parity) {
-      ok = ok && tc::mbar_wait_or(b, parity, gave_up);
+      ok = ok && tc::mbar_wait_or(b, parity, gave_up, p.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
     };
     // values nobody sees become 0, so that 0 * value is 0 whatever the slot held
@@ -827,7 +833,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           wait(bar->full + ks % Cfg::SLOTS, (ks / Cfg::SLOTS) & 1);
         }
         said ^= 1u << t;
-        if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
+        if (ok && lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
       }
       base += 2 * count;
     }
@@ -860,7 +866,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < cnt; ++i) {
         const int key0 = (w.k.t0 + w.first + (pair ? i : 2 * i + t)) * PA_KT;
-        ok = ok && tc::mbar_wait_or(bar->s_full + t, sc & 1, gave_up);
+        ok = ok && tc::mbar_wait_or(bar->s_full + t, sc & 1, gave_up, p.wait_ns);
         ++sc;
         ok = __all_sync(0xffffffffu, ok);
         if (work && ok) {
@@ -934,7 +940,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
               m = grow ? mt - PA_LIFT<T> : m;
               if (scale) {
                 if (hf == 1) {  // O must have the first half's products before it is scaled
-                  ok = ok && tc::mbar_wait_or(bar->half_done + t, (sc & 1) ^ 1, gave_up);
+                  ok = ok && tc::mbar_wait_or(bar->half_done + t, (sc & 1) ^ 1, gave_up, p.wait_ns);
                   ok = __all_sync(0xffffffffu, ok);
                   tc::fence_after_sync();
                 }
@@ -962,14 +968,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           }
         } else {
           tc::fence_before_sync();
-          if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
+          if (ok && lane == 0) tc::mbar_arrive(bar->p_full + 2 * t);
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar->p_full + 2 * t + 1);
+        if (ok && lane == 0) tc::mbar_arrive(bar->p_full + 2 * t + 1);
       }
       if (cnt > 0) {
-        ok = ok && tc::mbar_wait_or(bar->o_full + t, oc & 1, gave_up);
+        ok = ok && tc::mbar_wait_or(bar->o_full + t, oc & 1, gave_up, p.wait_ns);
         ++oc;
         ok = __all_sync(0xffffffffu, ok);
       }

@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cmath>
 
+#include "../../include/dg_ops.h"
 #include "dg_internal.h"
 #include "k_paged_attn.cuh"
 #include "k_paged_rows.cuh"
@@ -11,6 +12,10 @@
 using namespace dg;
 
 namespace {
+
+// dg_debug_stall_paged: this thread's next attention launch withholds its values, with waits
+// of this many ns (0: an ordinary launch)
+thread_local int64_t stall_ns = 0;
 
 int elem_size(int dtype) { return dtype == DG_ELEM_F32 ? 4 : 2; }
 
@@ -458,6 +463,9 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
   p.out = out;
   p.lse = lse;
   p.err = err;
+  p.wait_ns = stall_ns > 0 ? (uint64_t)stall_ns : 2000000000ull;
+  p.stall = stall_ns > 0;
+  stall_ns = 0;
   p.part_rows = piece_rows(batch, group);
   char* ws = static_cast<char*>(workspace);
   const size_t rows = (size_t)PA_CTAS * 2 * p.part_rows;
@@ -470,6 +478,13 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
                    : launch_attention<bf16, 128>(mq, mk, mv, p, st);
   return h == 64 ? launch_attention<__half, 64>(mq, mk, mv, p, st)
                  : launch_attention<__half, 128>(mq, mk, mv, p, st);
+}
+
+dg_status dg_debug_stall_paged(int64_t limit_ns) {
+  set_error("%s", "");
+  DG_REQUIRE(limit_ns >= 100000 && limit_ns <= 1000000000, "limit_ns outside [1e5, 1e9]");
+  stall_ns = limit_ns;
+  return DG_OK;
 }
 
 }  // extern "C"

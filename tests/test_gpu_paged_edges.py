@@ -175,3 +175,27 @@ def test_chunks_beyond_a_bound_of_no_rows_are_flagged():
         assert (int(a), int(b)) == (want, want)
         assert bool((mem == 7).all()) and torch.equal(pg.kmem, keep)
         pg.q_start.zero_()
+
+
+# ------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("dt,h,seqs,causal", [
+    (BF16, 128, [(1, 40)], True), (BF16, 128, [(1, 5000), (9, 9000)], True),
+    (F16, 64, [(300, 700), (1, 1000), (130, 130)], False), (BF16, 64, [(1, 90)] * 700, True)])
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_operator_usable(dt, h, seqs, causal):
+    """The values never come (the launch does not load them): the call ends by itself, says so,
+    and the calls after it have the bits of those before."""
+    pg = Pages(seqs, 2, h, 16, dt)
+    q = rnd(71, pg.n, 8, h, dt=dt)
+    want = binding.dg_paged_attention(pg.cache, pg.batch, q, causal)
+    for _ in range(2):
+        err = err_word()
+        binding.dg_debug_stall_paged(5_000_000)  # 5 ms a wait
+        binding.dg_paged_attention(pg.cache, pg.batch, q, causal, err=err)
+        with pytest.raises(binding.DGError, match="wait") as e:
+            binding.dg_paged_check(err)
+        assert e.value.status == 5 and int(err) == binding.PAGED_TIMEOUT
+        for _ in range(3):
+            err = err_word()
+            assert torch.equal(binding.dg_paged_attention(pg.cache, pg.batch, q, causal, err=err),
+                               want)
+            binding.dg_paged_check(err)

@@ -28,3 +28,29 @@ def test_scales_whose_exponents_overflow_are_refused(lib):
     # refused for its workspace instead, which is checked later
     assert attention(lib, scale=top / 1.4427, ws=None) == 1
     assert b"workspace" in lib.dg_last_error()
+
+
+def test_the_stall_hook_refuses_limits_that_are_no_test(lib):
+    for bad in (0, -1, 99_999, 1_000_000_001):
+        assert lib.dg_debug_stall_paged(bad) == 1 and lib.dg_last_error()
+
+
+class Word:
+    """Stands in for a device error word."""
+
+    def __init__(self, bits):
+        self.bits = bits
+
+    def item(self):
+        return self.bits
+
+
+@pytest.mark.parametrize("bits,status,text", [
+    (binding.PAGED_TIMEOUT, 5, "wait"), (7, 5, "wait"), (binding.PAGED_BAD_BATCH, 1, "kv_len"),
+    (binding.PAGED_BAD_PAGE, 1, "page number"), (3, 1, "page number")])
+def test_every_error_bit_is_reported(monkeypatch, bits, status, text):
+    monkeypatch.setattr(binding, "_arg", lambda *a: None)
+    binding.dg_paged_check(Word(0))
+    with pytest.raises(binding.DGError, match=text) as e:
+        binding.dg_paged_check(Word(bits))
+    assert e.value.status == status
