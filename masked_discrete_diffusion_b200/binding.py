@@ -702,7 +702,10 @@ def _bytes(stream, n: int, device):
 class PagedCache:
     """One layer's pages: k_pages and v_pages [n_pages, page_size, Hkv, h], bf16 or f16,
     of equal strides.  Any order of the first three axes in memory will do (a permuted
-    view, say); the channels are contiguous.  Keeps the tensors, copies nothing."""
+    view, say); the channels are contiguous.  Keeps the tensors, copies nothing.
+
+    err: a device int32 [1], zeroed here, that collects the PAGED_* bits of the calls on
+    this cache that name no err of their own (dg_paged_check reads and clears it)."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor):
         _cuda(k_pages, "k_pages", (torch.bfloat16, torch.float16), 4)
@@ -719,6 +722,8 @@ class PagedCache:
         self.n_kv_heads, self.head_dim, self.page_size = hkv, h, ps
         self.c = dg_paged_cache(k_pages.data_ptr(), v_pages.data_ptr(), _ELEMS[self.dtype], n,
                                 ps, hkv, h, sp, st, sh)
+        self.err = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
+        self._err = self.err.data_ptr()
 
 
 class PagedBatch:
@@ -816,7 +821,8 @@ def dg_paged_append(cache: PagedCache, batch: PagedBatch, k: torch.Tensor, v: to
     """Stores the chunk rows' keys k [n, Hkv, h] (normalised if eps is given, rotated to
     their positions if rope is) and values v into their pages; with q [n, Hq, h] also
     writes the normalised and rotated queries to q_out (may be q).  Returns q_out.
-    err: a device int32 [1] that collects PAGED_BAD_* bits (dg_paged_check)."""
+    err: a device int32 [1] that collects PAGED_BAD_* bits (dg_paged_check); cache.err
+    unless given."""
     dev = _device_of(cache, batch)
     h, dt, dts = cache.head_dim, cache.dtype, cache.dtypes
     kh = _heads(k, "k", dts, dev, None, h)
@@ -833,7 +839,8 @@ def dg_paged_append(cache: PagedCache, batch: PagedBatch, k: torch.Tensor, v: to
     _check(lib().dg_paged_append(
         ctypes.byref(cache.c), ctypes.byref(b), ctypes.byref(kh), ctypes.byref(vh),
         _opt_ref(rope), _full(k_gain, "k_gain", dt, dev, (h,)), _eps(eps), _opt_ref(qh),
-        _full(q_gain, "q_gain", dt, dev, (h,)), _opt_ref(qo), _full(err, "err", torch.int32, dev, (1,)),
+        _full(q_gain, "q_gain", dt, dev, (h,)), _opt_ref(qo),
+        cache._err if err is None else _full(err, "err", torch.int32, dev, (1,)),
         _raw_stream(stream, dev)))
     return q_out
 
@@ -845,7 +852,9 @@ def dg_paged_attention(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, ca
     [n, Hq, h].  causal: a bool, or a uint8 flag per sequence [B] (0: the chunk's rows see
     the whole chunk).  window: the positions back a causal row sees, itself included, or
     that a bidirectional chunk sees before itself (0: all).  scale: 1 / sqrt(h) unless
-    given.  lse: float32 [n, Hq] to receive the log of each row's sum of exponentials."""
+    given.  lse: float32 [n, Hq] to receive the log of each row's sum of exponentials.
+    err: as in dg_paged_append.  Rows of no sequence, or of one that err reports, are left as
+    they were: whatever the memory held where out was not given."""
     if not -0x80000000 <= window <= 0x7fffffff:  # ctypes would cut it: 2^32 to "no limit"
         raise ValueError("window outside [0, 2^31)")
     dev = _device_of(cache, batch)
@@ -864,7 +873,8 @@ def dg_paged_attention(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, ca
         ctypes.byref(cache.c), ctypes.byref(b), ctypes.byref(qh), 1 if causal else 0, flags,
         window, h ** -0.5 if scale is None else scale, _full(out, "out", dt, dev, (n, hq, h)),
         _full(lse, "lse", torch.float32, dev, (n, hq)), ws.data_ptr(), need,
-        _full(err, "err", torch.int32, dev, (1,)), _raw_stream(stream, dev)))
+        cache._err if err is None else _full(err, "err", torch.int32, dev, (1,)),
+        _raw_stream(stream, dev)))
     return out
 
 
@@ -873,10 +883,14 @@ def dg_debug_stall_paged(limit_ns: int):
     _check(lib().dg_debug_stall_paged(limit_ns))
 
 
-def dg_paged_check(err: torch.Tensor):
-    """Reads an err word (synchronising) and raises DGError if a bit is set."""
-    _arg(err, "err", torch.int32, (1,))
-    bits = int(err.item())
+def dg_paged_check(err):
+    """Reads an err word, or a PagedCache's own (synchronising with the current stream), and
+    raises DGError if a bit is set.  A cache's word is cleared by the report, a caller's not."""
+    word = err.err if isinstance(err, PagedCache) else err
+    _arg(word, "err", torch.int32, (1,))
+    bits = int(word.item())
+    if bits and word is not err:
+        word.zero_()
     if bits & PAGED_TIMEOUT:
         raise DGError(5, lib().dg_status_str(5).decode(), "a bounded device-side wait gave up")
     if bits:

@@ -199,3 +199,40 @@ def test_a_wait_that_runs_out_is_reported_and_leaves_the_operator_usable(dt, h, 
             assert torch.equal(binding.dg_paged_attention(pg.cache, pg.batch, q, causal, err=err),
                                want)
             binding.dg_paged_check(err)
+
+
+# ------------------------------------------------------------------ the cache's own error word
+def test_calls_without_an_err_report_to_their_cache():
+    pg, other = (Pages([(2, 40), (3, 20)], 2, 64, 16, BF16) for _ in range(2))
+    q, kv = rnd(81, 5, 4, 64), rnd(82, 5, 2, 64)
+
+    def both(p, err=None):
+        binding.dg_paged_append(p.cache, p.batch, kv, kv, err=err)
+        return binding.dg_paged_attention(p.cache, p.batch, q, err=err)
+
+    both(pg)
+    binding.dg_paged_check(pg.cache)
+    pg.table[1, 0] = -1
+    both(pg), both(other)
+    with pytest.raises(binding.DGError, match="page number"):
+        binding.dg_paged_check(pg.cache)
+    binding.dg_paged_check(pg.cache)     # the report has cleared it
+    binding.dg_paged_check(other.cache)  # and the other cache never saw it
+    mine = err_word()
+    both(pg, mine)
+    assert int(mine) == binding.PAGED_BAD_PAGE
+    binding.dg_paged_check(pg.cache)     # a caller's word is used instead
+    pg.kv_len[0] = 1000
+    binding.dg_paged_append(pg.cache, pg.batch, kv, kv)
+    with pytest.raises(binding.DGError, match="kv_len"):
+        binding.dg_paged_check(pg.cache)
+    # captured: every replay reports
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        both(pg)
+    binding.dg_paged_check(pg.cache)
+    for _ in range(2):
+        graph.replay()
+        with pytest.raises(binding.DGError, match="kv_len"):
+            binding.dg_paged_check(pg.cache)
