@@ -28,7 +28,7 @@ int ilog2(int x) {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Strides that reach a row's last byte without leaving 63 bits, each a multiple of 16 bytes.
-dg_status check_heads(const dg_heads* x, const char* what, long long n, int h, int esz) {
+dg_status check_heads(const dg_heads* x, const char* what, long long n, int esz) {
   DG_REQUIRE(x->n_heads >= 0 && x->n_heads <= 65536, "%s: n_heads=%d outside [0, 65536]", what,
              x->n_heads);
   if (n == 0 || x->n_heads == 0) return DG_OK;
@@ -41,13 +41,12 @@ dg_status check_heads(const dg_heads* x, const char* what, long long n, int h, i
   DG_REQUIRE((n == 1 || x->token_stride * esz % 16 == 0) &&
                  (x->n_heads == 1 || x->head_stride * esz % 16 == 0),
              "%s: strides must be multiples of 16 bytes", what);
-  (void)h;
   return DG_OK;
 }
 
 // An output additionally has no two rows on the same memory.
 dg_status check_out_heads(const dg_heads* x, const char* what, long long n, int h, int esz) {
-  DG_TRY(check_heads(x, what, n, h, esz));
+  DG_TRY(check_heads(x, what, n, esz));
   if (n == 0 || x->n_heads == 0) return DG_OK;
   const long long t = x->token_stride, j = x->head_stride;
   const bool token_outer = (x->n_heads == 1 || j >= h) &&
@@ -137,7 +136,7 @@ dg_status launch_status(cudaError_t e, const char* what) {
 }
 
 // A head takes h/16 lanes; a warp takes as many groups of heads as leave the device enough
-// warps, since the sines are computed once per warp and row.
+// warps (32 an SM), since the sines are computed once per warp and row.
 template <class T, bool APPEND>
 dg_status launch_rows(RowsParams& p, const dg_rope* rope, cudaStream_t st, const char* what) {
   p.lg = 0;
@@ -145,7 +144,7 @@ dg_status launch_rows(RowsParams& p, const dg_rope* rope, cudaStream_t st, const
   const int per = 32 >> p.lg;
   const int groups = (p.hq + per - 1) / per + (APPEND ? 2 : 1) * ((p.hkv + per - 1) / per);
   p.iters = 1;
-  while (p.iters < groups && (long long)p.n * ((groups + p.iters - 1) / p.iters) > 148 * 32)
+  while (p.iters < groups && (long long)p.n * ((groups + p.iters - 1) / p.iters) > PA_CTAS * 32)
     ++p.iters;
   p.parts = (groups + p.iters - 1) / p.iters;
   p.inv_h = 1.0f / (float)p.h;
@@ -283,8 +282,8 @@ dg_status dg_qk_norm_rope(int32_t dtype, int32_t n, int32_t head_dim, const dg_h
   DG_REQUIRE(q->n_heads == q_out->n_heads && k->n_heads == k_out->n_heads,
              "outputs must have their inputs' heads");
   const int esz = elem_size(dtype);
-  DG_TRY(check_heads(q, "q", n, head_dim, esz));
-  DG_TRY(check_heads(k, "k", n, head_dim, esz));
+  DG_TRY(check_heads(q, "q", n, esz));
+  DG_TRY(check_heads(k, "k", n, esz));
   DG_TRY(check_out_heads(q_out, "q_out", n, head_dim, esz));
   DG_TRY(check_out_heads(k_out, "k_out", n, head_dim, esz));
   DG_TRY(check_norm(q_gain, k_gain, eps));
@@ -326,11 +325,11 @@ dg_status dg_paged_append(const dg_paged_cache* cache, const dg_paged_batch* bat
   DG_REQUIRE(!q == !q_out, "q and q_out go together");
   DG_REQUIRE(q || !q_gain, "q_gain without q");
   const int h = cache->head_dim, n = batch->n_tokens;
-  DG_TRY(check_heads(k, "k", n, h, 2));
-  DG_TRY(check_heads(v, "v", n, h, 2));
+  DG_TRY(check_heads(k, "k", n, 2));
+  DG_TRY(check_heads(v, "v", n, 2));
   if (q) {
     DG_REQUIRE(q->n_heads == q_out->n_heads, "q_out must have q's heads");
-    DG_TRY(check_heads(q, "q", n, h, 2));
+    DG_TRY(check_heads(q, "q", n, 2));
     DG_TRY(check_out_heads(q_out, "q_out", n, h, 2));
   }
   DG_TRY(check_norm(q_gain, k_gain, eps));
@@ -402,7 +401,7 @@ dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* 
     set_error("paged attention needs at most 128 query heads a key head, not %d", group);
     return DG_ERR_UNSUPPORTED;
   }
-  DG_TRY(check_heads(q, "q", n, h, 2));
+  DG_TRY(check_heads(q, "q", n, 2));
   DG_REQUIRE(window >= 0, "negative window");
   const float scale_log2 = scale * 1.4426950408889634f;  // the kernel's: exponents of 2
   DG_REQUIRE(std::isfinite(scale_log2) && scale > 0.f,
