@@ -22,6 +22,8 @@
  *     or written.
  *   - Rows that belong to no sequence (before q_start[0], from q_start[B] on) are left as
  *     they were in every output, and so are the rows of a sequence with a bad length.
+ *   - A call with no rows (n or n_tokens 0) or no sequence (B 0) does nothing, and looks at
+ *     nothing on the device.
  */
 #ifndef DG_PAGED_H
 #define DG_PAGED_H
@@ -90,7 +92,8 @@ dg_status dg_rope_init(double base, int32_t head_dim, dg_rope* out);
 
 /* Per head row x of q and of k: y = x / sqrt(mean(x^2) + eps) * gain (eps < 0: y = x, and
  * the gains must be NULL; a NULL gain is 1), then the rotation of y to positions[t]
- * (rope: host pointer, NULL: none).  Sums and angles in fp32 or better, one rounding at
+ * (rope: host pointer, NULL: none).  Squares, sums and angles in fp32 or better (a row
+ * whose squares leave fp32's range, elements beyond 2^60, comes out as 0), one rounding at
  * the end.  q_out and k_out have q's and k's shapes and may be the same memory as their
  * inputs; otherwise they must not overlap them.  k->n_heads may be 0 (k_out then unused),
  * and so may q's.  q_gain, k_gain: [head_dim] of the rows' type, 16-byte aligned.
@@ -126,14 +129,15 @@ dg_status dg_paged_attention_workspace(const dg_paged_cache* cache, const dg_pag
  *     it (the canvas rows of dg.h).  window 0: no limit.
  * A row that sees nothing gets 0 and lse -inf.  lse (nullable): [n_tokens, Hq] fp32, the
  * natural log of the sum of exponentials.  out: [n_tokens, Hq, head_dim] of the cache's
- * type, contiguous, 16-byte aligned.  Scores, softmax and sums are fp32; the weights are
+ * type, contiguous, 16-byte aligned, overlapping no input.  Scores, softmax and sums are fp32; the weights are
  * rounded to the cache's type before they meet the values (f16: by at most 2^-32 of the
  * row's largest weight where that is more than half a step of the weight itself).
  * Keys and values at positions no row of the sequence sees, slots past kv_len included,
  * may hold anything; a non-finite value that some row sees can reach other rows of the same
  * sequence.  workspace: 256-byte aligned, at least dg_paged_attention_workspace bytes, this
  * call's alone until it has finished; it needs no initial value.
- * Requires head_dim 64 or 128, Hq a multiple of Hkv with Hq / Hkv <= 128, scale > 0 and
+ * Requires head_dim 64 or 128 (dg_paged_append stores heads of other sizes too, for other
+ * readers), Hq a multiple of Hkv with Hq / Hkv <= 128, scale > 0 and
  * scale log2(e) finite in fp32, window >= 0, q's strides > 0 where it has more than one row or head, max_pages *
  * page_size at least 256 below 2^31, and fewer than 2^31 key tiles of 128 in all (chunk rows
  * by key heads, against the table's width: DG_ERR_UNSUPPORTED). */

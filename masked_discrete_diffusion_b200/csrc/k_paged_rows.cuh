@@ -4,7 +4,9 @@
 // A head row x of h channels becomes y = x * rsqrt(mean(x^2) + eps) * gain, then pair
 // (i, i + h/2) turns by position * base^(-2i/h).  The angle is kept in turns: position
 // times the pair's 64-bit fraction of a turn, modulo 2^64, is exact, and its top 32 bits go
-// through sincospif, so position 2^30 costs no more precision than position 1.
+// through sincospif, so position 2^30 costs no more precision than position 1.  sincospif
+// takes a float: the angle is cut to 24 bits, at most 2^-25 half turns (9e-8 radians), below
+// what 16-bit rows resolve and on a level with the rounding of f32 ones.
 //
 // Bound by memory: each element is read once and written once, with ~10 operations on it.
 // A head is held by h/16 lanes (rounded up to a power of two), each with channels
