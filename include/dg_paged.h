@@ -129,16 +129,17 @@ dg_status dg_paged_attention_workspace(const dg_paged_cache* cache, const dg_pag
  *     it (the canvas rows of dg.h).  window 0: no limit.
  * A row that sees nothing gets 0 and lse -inf.  lse (nullable): [n_tokens, Hq] fp32, the
  * natural log of the sum of exponentials.  out: [n_tokens, Hq, head_dim] of the cache's
- * type, contiguous, 16-byte aligned, overlapping no input.  Scores, softmax and sums are fp32; the weights are
- * rounded to the cache's type before they meet the values (f16: by at most 2^-32 of the
- * row's largest weight where that is more than half a step of the weight itself).
+ * type, contiguous, 16-byte aligned, overlapping no input.  Scores, softmax and sums are
+ * fp32; the weights are rounded to the cache's type before they meet the values (f16: by at
+ * most 2^-32 of the row's largest weight where that is more than half a step of the weight
+ * itself).
  * Keys and values at positions no row of the sequence sees, slots past kv_len included,
  * may hold anything; a non-finite value that some row sees can reach other rows of the same
  * sequence.  workspace: 256-byte aligned, at least dg_paged_attention_workspace bytes, this
  * call's alone until it has finished; it needs no initial value.
  * Requires head_dim 64 or 128 (dg_paged_append stores heads of other sizes too, for other
- * readers), Hq a multiple of Hkv with Hq / Hkv <= 128, scale > 0 and
- * scale log2(e) finite in fp32, window >= 0, q's strides > 0 where it has more than one row or head, max_pages *
+ * readers), Hq a multiple of Hkv with Hq / Hkv <= 128, scale > 0 and scale log2(e) finite in
+ * fp32, window >= 0, q's strides > 0 where it has more than one row or head, max_pages *
  * page_size at least 256 below 2^31, and fewer than 2^31 key tiles of 128 in all (chunk rows
  * by key heads, against the table's width: DG_ERR_UNSUPPORTED). */
 dg_status dg_paged_attention(const dg_paged_cache* cache, const dg_paged_batch* batch,

@@ -37,12 +37,12 @@
 // Bound.  Single tokens and drafts read each visible key and value once: memory (64 sequences
 // of up to 16,384 keys: 203 us for 1.24 GB, 6.1 TB/s, 0.93 of the measured copy rate, from
 // pages of 16 tokens, 2 KB a box; 237 us, 5.2 TB/s, 0.80 in a loop of a second, in which the
-// power cap takes the SMs to 1,480 MHz).  Long chunks: a pair of tiles (128 keys of 2 x 128 rows) takes
-// the tensor cores 2,050 cycles and the SFU's exponentials as long; here it takes about 3,200,
-// since a stream's next scores need the columns its weights stand in, so that softmax and
-// products of one stream follow each other (8,192 causal tokens, 16 heads of 128: 240 to 253 us,
-// 1,090 to 1,150 TFLOP/s, 0.66 to 0.69 of the measured cuBLAS burst rate; 276 us, 996 TFLOP/s,
-// 0.60 in a loop of a second, at 1,640 MHz).  Short work: the first scores come
+// power cap takes the SMs to 1,480 MHz).  Long chunks: a pair of tiles (128 keys of 2 x 128
+// rows) takes the tensor cores 2,050 cycles and the SFU's exponentials as long; here it takes
+// about 3,200, since a stream's next scores need the columns its weights stand in, so that
+// softmax and products of one stream follow each other (8,192 causal tokens, 16 heads of 128:
+// 240 to 250 us, 1,100 to 1,150 TFLOP/s, 0.66 to 0.69 of the measured cuBLAS burst rate; 276 us,
+// 996 TFLOP/s, 0.60 in a loop of a second, at 1,640 MHz).  Short work: the first scores come
 // 9,500 cycles after the start (lengths, plan, page table, keys, and instructions that no one
 // has run yet), the last rows leave 4,000 after theirs.
 #pragma once
